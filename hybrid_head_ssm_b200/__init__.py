@@ -46,6 +46,7 @@ HYMBA_MODE_PREFILL = 0
 HYMBA_MODE_DECODE = 1
 
 _i32, _f32, _vp, _sz = ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+_i64 = ctypes.c_int64
 
 
 class hymba_layer_cfg(ctypes.Structure):
@@ -77,6 +78,21 @@ class hymba_ssm_state(ctypes.Structure):
     _fields_ = [("h", _vp), ("conv", _vp)]
 
 
+class hymba_attn_shape(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("n_q_heads", "n_kv_heads", "head_dim", "v_head_dim", "n_meta", "window",
+                                    "dtype")] + [("scale", _f32)]
+
+
+class hymba_paged_kv(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("k_pages", "v_pages", "page_table", "len")] + [
+        (n, _i32) for n in ("n_pages", "page_size", "max_pages", "batch", "n_kv_heads", "head_dim", "v_head_dim",
+                            "dtype")]
+
+
+class hymba_linattn_shape(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("n_qk_heads", "n_heads", "key_dim", "v_head_dim", "dtype")] + [("scale", _f32)]
+
+
 _P = ctypes.POINTER
 _sig = {
     "hymba_mixer_prefill": (ctypes.c_int, [_P(hymba_layer_cfg), _P(hymba_layer_weights), _vp, ctypes.c_int,
@@ -104,6 +120,17 @@ _sig = {
     "hymba_launch_count": (ctypes.c_uint64, []),
     "hymba_attn_decode_static": (ctypes.c_int, [_P(hymba_layer_cfg), _vp, ctypes.c_int64, _P(hymba_kv), _vp,
                                                 ctypes.c_int, _vp]),
+    "hymba_attn_prefill_packed": (ctypes.c_int, [_P(hymba_attn_shape), _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                                 ctypes.c_int, ctypes.c_int, _vp, _i64, _vp]),
+    "hymba_kv_append_paged": (ctypes.c_int, [_P(hymba_paged_kv), _vp, _i64, _vp, _i64, _vp, ctypes.c_int, _vp]),
+    "hymba_attn_decode_paged": (ctypes.c_int, [_P(hymba_attn_shape), _vp, _i64, _P(hymba_paged_kv), ctypes.c_int,
+                                               _vp, _i64, _vp, _sz, _vp]),
+    "hymba_attn_decode_paged_workspace": (_sz, [_P(hymba_attn_shape), ctypes.c_int, ctypes.c_int]),
+    "hymba_linattn_prefill": (ctypes.c_int, [_P(hymba_linattn_shape), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                             _vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
+    "hymba_linattn_workspace": (_sz, [_P(hymba_linattn_shape), ctypes.c_int, ctypes.c_int]),
+    "hymba_linattn_step": (ctypes.c_int, [_P(hymba_linattn_shape), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                          ctypes.c_int, _vp, _i64, _vp]),
     "hymba_probe_unit_rates": (ctypes.c_int, [_P(ctypes.c_double), ctypes.c_int, _vp]),
     "hymba_debug_set_wait_limit": (ctypes.c_int, [ctypes.c_longlong]),
     "hymba_debug_stalled_wait": (ctypes.c_int, [_vp]),
@@ -189,6 +216,18 @@ def kv_struct(cfg, batch: int, k_seq=None, v_seq=None, k_cache=None, v_cache=Non
 
 def state_struct(h=None, conv=None) -> hymba_ssm_state:
     return hymba_ssm_state(h=_ptr(h), conv=_ptr(conv))
+
+
+def attn_shape(n_q_heads: int, n_kv_heads: int, head_dim: int, v_head_dim: int, n_meta: int = 0, window: int = 0,
+               dtype: int = HYMBA_F16, scale: float = 0.0) -> hymba_attn_shape:
+    """Attention heads of a ragged batch (scale 0: 1 / sqrt(head_dim))."""
+    return hymba_attn_shape(n_q_heads, n_kv_heads, head_dim, v_head_dim, n_meta, window, dtype, scale)
+
+
+def linattn_shape(n_qk_heads: int, n_heads: int, key_dim: int, v_head_dim: int, dtype: int = HYMBA_F16,
+                  scale: float = 0.0) -> hymba_linattn_shape:
+    """Linear-attention heads of a ragged batch (scale 0: 1 / sqrt(key_dim))."""
+    return hymba_linattn_shape(n_qk_heads, n_heads, key_dim, v_head_dim, dtype, scale)
 
 
 def current_stream_ptr():

@@ -1,0 +1,202 @@
+// Causal attention over packed prompts on CUDA cores (fp32 rows): softmax(scale q k^T) v
+// with grouped heads, meta prefix + window or the whole history, counted from each
+// sequence's first row ("Jamba: Hybrid SSM-Transformer", section 1; "Hymba Guide",
+// Learnable Meta-Tokens; 51cto Hymba-1.5B article, section 2).
+//
+// One 256-thread block per (64 query rows of a sequence, head), the heaviest rows of a
+// sequence first. Key tiles of 64: S (64 x 64) as 4 x 4 per thread from transposed Q and K
+// tiles, one running max and sum per row, P transposed through shared memory, O as 4 rows
+// x DV/16 columns per thread. Bound by the FMA pipe: 2 (dh + dv) flops per visible pair,
+// and the diagonal tiles' masked half on top.
+#include "kernels.h"
+#include "ragged.cuh"
+
+namespace hymba {
+
+namespace {
+
+constexpr int QT = 64, KT = 64, LD = QT + 4, NT = 256;
+
+template <int DH, int DV>
+struct PackedSimtSmem {
+    alignas(16) float q[DH][LD];  // transposed: [dim][row]
+    alignas(16) float k[DH][LD];  // transposed: [dim][key]
+    alignas(16) float v[KT][DV];
+    alignas(16) float p[KT][LD];  // transposed: [key][row]
+    ragged::FindSmem find;
+};
+
+template <typename T, int DH, int DV>
+__global__ void __launch_bounds__(NT)
+attn_packed_simt_kernel(const T* __restrict__ q, long long ldq, const T* __restrict__ k, long long ldk,
+                        const T* __restrict__ v, long long ldv, const int* __restrict__ cu, int n_seqs, int total,
+                        T* __restrict__ o, long long ldo, int H, int G, int n_meta, int window, float scale_log2,
+                        int* status) {
+    griddep_sync();
+    extern __shared__ __align__(16) uint8_t packed_simt_raw[];
+    PackedSimtSmem<DH, DV>& sm = *reinterpret_cast<PackedSimtSmem<DH, DV>*>(packed_simt_raw);
+    const int h = blockIdx.x % H, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const ragged::Item it = ragged::find_item<NT>(sm.find, cu, n_seqs, total, QT, false, blockIdx.x / H, status);
+    if (it.seq < 0) return;
+    const int L = it.len;
+    const int i0 = ((L + QT - 1) / QT - 1 - it.tile) * QT;
+    const long long row0 = it.start;
+    const int g = h / (H / G);
+    q += row0 * ldq + (long long)h * DH;
+    k += row0 * ldk + (long long)g * DH;
+    v += row0 * ldv + (long long)g * DV;
+
+    for (int j = tid; j < QT * (DH / 8); j += NT) {
+        const int r = j % QT, c = j / QT;
+        float x[8];
+        ragged::load8(q + (long long)min(i0 + r, L - 1) * ldq + 8 * c, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sm.q[8 * c + e][r] = x[e] * scale_log2;
+    }
+    float acc[4][DV / 16], mrun[4], l[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        mrun[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int c = 0; c < DV / 16; ++c) acc[r][c] = 0.f;
+    }
+    const int i_last = min(i0 + QT, L) - 1;
+    const int lo = window > 0 ? max(n_meta, i0 - window + 1) : n_meta;
+    for (int range = 0; range < 2; ++range) {
+        const int end = range == 0 ? min(n_meta, i_last + 1) : i_last + 1;
+        for (int j0 = range == 0 ? 0 : lo; j0 < end; j0 += KT) {
+            __syncthreads();
+            int odd = 0;  // a value of V that is not finite: the product may not meet it where it is masked
+            for (int j = tid; j < KT * (DH / 8); j += NT) {
+                const int r = j % KT, c = j / KT;
+                float x[8] = {};
+                if (j0 + r < end) ragged::load8(k + (long long)(j0 + r) * ldk + 8 * c, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sm.k[8 * c + e][r] = x[e];
+            }
+            for (int j = tid; j < KT * (DV / 8); j += NT) {
+                const int c = j % (DV / 8), r = j / (DV / 8);
+                float x[8] = {};
+                if (j0 + r < end) ragged::load8(v + (long long)(j0 + r) * ldv + 8 * c, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) odd |= !isfinite(x[e]);
+                *reinterpret_cast<float4*>(&sm.v[r][8 * c]) = make_float4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<float4*>(&sm.v[r][8 * c + 4]) = make_float4(x[4], x[5], x[6], x[7]);
+            }
+            odd = __syncthreads_or(odd);
+            float s[4][4] = {};
+#pragma unroll 8
+            for (int d = 0; d < DH; ++d) {
+                const float4 a = *reinterpret_cast<const float4*>(&sm.q[d][4 * ty]);
+                const float4 b = *reinterpret_cast<const float4*>(&sm.k[d][4 * tx]);
+                const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[r][c] = fmaf(av[r], bv[c], s[r][c]);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = i0 + 4 * ty + r;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int j = j0 + 4 * tx + c;
+                    const bool see = j < end && j <= i && (range == 0 || window <= 0 || i - j < window);
+                    s[r][c] = see ? s[r][c] : -INFINITY;
+                    mx = fmaxf(mx, s[r][c]);
+                }
+#pragma unroll
+                for (int w = 1; w < 16; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+                const float m = fmaxf(mrun[r], mx), mu = m == -INFINITY ? 0.f : m;
+                const float f = exp2f(mrun[r] - mu);
+                mrun[r] = m;
+                float sum = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    s[r][c] = exp2f(s[r][c] - mu);
+                    sum += s[r][c];
+                }
+                l[r] = l[r] * f + sum;  // this thread's columns; the 16 threads of the row are added at the end
+#pragma unroll
+                for (int c = 0; c < DV / 16; ++c) acc[r][c] *= f;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<float4*>(&sm.p[4 * tx + c][4 * ty]) = make_float4(s[0][c], s[1][c], s[2][c], s[3][c]);
+            __syncthreads();
+            const int nk = min(KT, end - j0);
+#pragma unroll 4
+            for (int j = 0; j < nk; ++j) {
+                const float4 a = *reinterpret_cast<const float4*>(&sm.p[j][4 * ty]);
+                const float av[4] = {a.x, a.y, a.z, a.w};
+                bool see[4] = {true, true, true, true};
+                if (odd) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int i = i0 + 4 * ty + r, jj = j0 + j;
+                        see[r] = jj <= i && (range == 0 || window <= 0 || i - jj < window);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < DV / 64; ++u) {
+                    const float4 b = *reinterpret_cast<const float4*>(&sm.v[j][4 * tx + 64 * u]);
+                    const float bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            acc[r][4 * u + c] = see[r] ? fmaf(av[r], bv[c], acc[r][4 * u + c]) : acc[r][4 * u + c];
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int i = i0 + 4 * ty + r;
+        float sum = l[r];
+#pragma unroll
+        for (int w = 1; w < 16; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+        // (a NaN sum divides: a visible NaN reaches its row)
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (i < L) {
+            T* dst = o + (row0 + i) * ldo + (long long)h * DV + 4 * tx;
+#pragma unroll
+            for (int u = 0; u < DV / 64; ++u)
+                ragged::store4(dst + 64 * u, acc[r][4 * u] * inv, acc[r][4 * u + 1] * inv, acc[r][4 * u + 2] * inv,
+                               acc[r][4 * u + 3] * inv);
+        }
+    }
+}
+
+template <typename T, int DH, int DV>
+int launch_dims(const Ctx& ctx, const PackedAttn& a) {
+    auto kern = attn_packed_simt_kernel<T, DH, DV>;
+    const size_t smem = sizeof(PackedSimtSmem<DH, DV>);
+    static std::atomic<unsigned long long> smem_set{0};
+    if (!smem_opt_in_once(smem_set, kern, smem, ctx)) return HYMBA_ERR_CUDA;
+    const long long blocks = ((long long)ceil_div(a.total, QT) + a.n_seqs) * a.H;
+    if (blocks > 0x7fffffffLL) return HYMBA_ERR_UNSUPPORTED;
+    HYMBA_LAUNCH(ctx, "attn_packed", kern, (unsigned)blocks, NT, smem, static_cast<const T*>(a.q), a.ldq,
+                 static_cast<const T*>(a.k), a.ldk, static_cast<const T*>(a.v), a.ldv, a.cu, a.n_seqs, a.total,
+                 static_cast<T*>(a.o), a.ldo, a.H, a.G, a.n_meta, a.window, a.scale * 1.4426950408889634f, ctx.status);
+    return HYMBA_OK;
+}
+
+}  // namespace
+
+template <typename T>
+int launch_attn_packed_simt(const Ctx& ctx, const PackedAttn& a) {
+    if (a.dh == 64 && a.dv == 64) return launch_dims<T, 64, 64>(ctx, a);
+    if (a.dh == 64 && a.dv == 128) return launch_dims<T, 64, 128>(ctx, a);
+    if (a.dh == 128 && a.dv == 64) return launch_dims<T, 128, 64>(ctx, a);
+    if (a.dh == 128 && a.dv == 128) return launch_dims<T, 128, 128>(ctx, a);
+    return HYMBA_ERR_UNSUPPORTED;
+}
+
+template int launch_attn_packed_simt<float>(const Ctx&, const PackedAttn&);
+template int launch_attn_packed_simt<f16>(const Ctx&, const PackedAttn&);
+template int launch_attn_packed_simt<bf16>(const Ctx&, const PackedAttn&);
+
+}  // namespace hymba

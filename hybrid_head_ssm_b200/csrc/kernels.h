@@ -130,4 +130,43 @@ int launch_ssm_decode(const Ctx& ctx, const T* P, long long ldP, int col_x, int 
                       const float* conv_w, const float* conv_b, const float* A_log, const float* D,
                       float* h, float* conv, T* ypre, int B, int di, int hp);
 
+// Attention over packed prompts: rows q, k, v -> o (row strides in elements), sequence
+// offsets cu [n_seqs + 1] within total rows.
+struct PackedAttn {
+    const void *q, *k, *v;
+    void* o;
+    long long ldq, ldk, ldv, ldo;
+    const int* cu;
+    int n_seqs, total, H, G, dh, dv, n_meta, window;
+    float scale;
+};
+// CUDA cores (fp32 rows)
+template <typename T>
+int launch_attn_packed_simt(const Ctx& ctx, const PackedAttn& a);
+
+// New rows into pages (elements of esz bytes); cu NULL: one row per sequence.
+int launch_kv_append(const Ctx& ctx, const hymba_paged_kv& kv, int esz, const void* k, long long ldk, const void* v,
+                     long long ldv, const int* cu, int rows);
+
+// Attention of the newest position of every sequence over its pages; partial results of
+// the key splits in ws (decode_paged_bytes).
+size_t decode_paged_bytes(const hymba_attn_shape& s, int batch, int max_len);
+int launch_decode_paged(const Ctx& ctx, const hymba_attn_shape& s, float scale, const void* q, long long ldq,
+                        const hymba_paged_kv& kv, int max_len, void* o, long long ldo, void* ws);
+
+// Linear attention with a decay per head: the recurrence S_t = exp(g_t) S_{t-1} + v_t
+// k_t^T, o_t = scale S_t q_t over packed rows (cu NULL: one row per sequence).
+struct LinAttn {
+    const void *q, *k, *v;
+    void* o;
+    long long ldq, ldk, ldv, ldo, ldg;
+    const float *g, *state_in;
+    float* state_out;
+    const int* cu;
+    int n_seqs, total, Hk, H, dk, dv;
+    float scale;
+};
+template <typename T>
+int launch_linattn_recurrent(const Ctx& ctx, const LinAttn& a);
+
 }  // namespace hymba

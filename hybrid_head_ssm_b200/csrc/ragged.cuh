@@ -1,0 +1,117 @@
+// Pieces shared by the kernels of ragged batches (packed prompts, paged K/V, linear
+// attention): work items of packed sequences, 16-byte row loads, fragments of either
+// 16-bit type.
+#pragma once
+#include "common.cuh"
+#include "warp_mma.cuh"
+
+namespace hymba {
+namespace ragged {
+
+// One work item of a packed batch: `tile`-th run of rows of sequence `seq`, whose rows
+// are start .. start + len - 1. seq < 0: no such item.
+struct Item {
+    int seq, start, len, tile;
+};
+
+// Sequence s of the packed batch; false when its offsets are out of order or out of range.
+__device__ __forceinline__ bool sequence(const int* cu, int s, int total, int* start, int* len) {
+    const int a = cu[s], b = cu[s + 1];
+    *start = a;
+    *len = b - a;
+    return a >= 0 && b >= a && b <= total;
+}
+
+struct FindSmem {
+    long long warp_sum[32];
+    Item item;
+};
+
+// The t-th work item when every sequence is cut into ceil(len / rows) runs (min_one: at
+// least one, so that empty sequences are items too). Called by all NT threads of the
+// block; each thread counts a run of consecutive sequences and one block scan finds the
+// sequence, so the cost is a few memory round trips for any number of sequences.
+template <int NT>
+__device__ Item find_item(FindSmem& sm, const int* cu, int n_seqs, int total, int rows, bool min_one, long long t,
+                          int* status) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (n_seqs + NT - 1) / NT;
+    const int s0 = min(tid * per, n_seqs), s1 = min(s0 + per, n_seqs);
+    if (tid == 0) sm.item.seq = -1;
+    long long mine = 0;
+    for (int s = s0; s < s1; ++s) {
+        int a, n;
+        if (sequence(cu, s, total, &a, &n)) {
+            const int c = (n + rows - 1) / rows;
+            mine += min_one && c == 0 ? 1 : c;
+        } else if (blockIdx.x == 0) {
+            set_status(status, HYMBA_ERR_DEVICE_RANGE);
+        }
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+    }
+    if (lane == 31) sm.warp_sum[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine;
+    for (int w = 0; w < warp; ++w) before += sm.warp_sum[w];
+    if (t >= before && t < before + mine) {
+        for (int s = s0; s < s1; ++s) {
+            int a, n;
+            if (!sequence(cu, s, total, &a, &n)) continue;
+            int c = (n + rows - 1) / rows;
+            if (min_one && c == 0) c = 1;
+            if (t < before + c) {
+                sm.item.seq = s;
+                sm.item.start = a;
+                sm.item.len = n;
+                sm.item.tile = (int)(t - before);
+                break;
+            }
+            before += c;
+        }
+    }
+    __syncthreads();
+    return sm.item;
+}
+
+// 8 consecutive elements as fp32 (one or two 16-byte loads)
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        const T* h = reinterpret_cast<const T*>(&u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f(h[i]);
+    } else {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+}
+
+// 4 consecutive elements as fp32 (one 8- or 16-byte load), and their store
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p) {
+    if constexpr (sizeof(T) == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        const T* h = reinterpret_cast<const T*>(&u);
+        return make_float4(to_f(h[0]), to_f(h[1]), to_f(h[2]), to_f(h[3]));
+    } else {
+        return *reinterpret_cast<const float4*>(p);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float a, float b, float c, float d) {
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(a, b), pack2<T>(c, d));
+    } else {
+        *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+    }
+}
+
+}  // namespace ragged
+}  // namespace hymba

@@ -11,9 +11,11 @@ from typing import Dict, Optional
 import numpy as np
 import torch
 
-from . import (HYMBA_BF16, HYMBA_MODE_DECODE, HYMBA_MODE_PREFILL, check, cfg_struct,
-               current_stream_ptr, hymba_mixer_decode, hymba_mixer_prefill, hymba_workspace_bytes,
-               kv_struct, state_struct, weights_struct)
+from . import (HYMBA_BF16, HYMBA_F16, HYMBA_F32, HYMBA_MODE_DECODE, HYMBA_MODE_PREFILL, check, cfg_struct,
+               current_stream_ptr, hymba_attn_decode_paged, hymba_attn_decode_paged_workspace,
+               hymba_attn_prefill_packed, hymba_kv_append_paged, hymba_linattn_prefill, hymba_linattn_step,
+               hymba_linattn_workspace, hymba_mixer_decode, hymba_mixer_prefill, hymba_paged_kv,
+               hymba_workspace_bytes, kv_struct, state_struct, weights_struct)
 
 BIG = ("w_in", "w_dt", "w_out", "meta")
 NAMES = ("w_in", "w_dt", "b_dt", "conv_w", "conv_b", "A_log", "D", "norm_attn_w", "norm_ssm_w",
@@ -133,3 +135,171 @@ def mlp(m: DeviceMLP, h: torch.Tensor, ws: torch.Tensor) -> None:
     rows = h.numel() // m.cfg.d_model
     check(hymba_mlp(ctypes.byref(m.c), m.d_ff, ctypes.byref(m.s), h.data_ptr(), rows, ws.data_ptr(), ws.numel(),
                     current_stream_ptr()))
+
+
+# ---------------------------------------------------------------------------
+# ragged batches: packed prompts, paged K/V, linear attention
+# ---------------------------------------------------------------------------
+TORCH_DTYPE = {HYMBA_F16: torch.float16, HYMBA_BF16: torch.bfloat16, HYMBA_F32: torch.float32}
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(name: str, t: torch.Tensor, width: int, code: int, dev: torch.device) -> int:
+    """Row stride of a [rows, width] tensor of one type on one device, its elements side by
+    side within a row."""
+    if t.dim() != 2 or t.shape[1] != width or t.dtype is not TORCH_DTYPE.get(code) or t.device != dev:
+        raise ValueError(f"{name}: [rows, {width}] of {TORCH_DTYPE.get(code)} on {dev} wanted, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must lie side by side")
+    # the stride of a single row is never used (and torch may report anything for it)
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _ints(name: str, t: torch.Tensor, shape, dev: torch.device) -> None:
+    if t.dtype is not torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name}: contiguous int32 {tuple(shape)} on {dev} wanted, got {tuple(t.shape)} of "
+                         f"{t.dtype} on {t.device}")
+
+
+def _floats(name: str, t: torch.Tensor, shape, dev: torch.device) -> None:
+    if t.dtype is not torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name}: contiguous float32 {tuple(shape)} on {dev} wanted, got {tuple(t.shape)} of "
+                         f"{t.dtype} on {t.device}")
+
+
+def _queue(dev: torch.device, fn, *args) -> None:
+    """Call fn(*args, stream) with the tensors' device current, on torch's current stream
+    of that device."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        check(fn(*args, stream))
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args, stream))
+
+
+class PagedKV:
+    """K and V in pages: k_pages [n_pages, n_kv_heads, page_size, head_dim], v_pages [n_pages,
+    n_kv_heads, page_size, v_head_dim], page_table int32 [batch, max_pages], len int32
+    [batch]; the tensors stay the caller's and are kept alive here."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, length: torch.Tensor):
+        code = {v: k for k, v in TORCH_DTYPE.items()}.get(k_pages.dtype)
+        dev = k_pages.device
+        _need(code is not None and k_pages.dim() == 4 and k_pages.is_contiguous(),
+              "k_pages: contiguous [n_pages, n_kv_heads, page_size, head_dim] of float16, bfloat16 or float32")
+        _need(v_pages.dim() == 4 and v_pages.is_contiguous() and v_pages.shape[:3] == k_pages.shape[:3]
+              and v_pages.dtype is k_pages.dtype and v_pages.device == dev,
+              "v_pages: contiguous, with k_pages' pages, heads, page size, type and device")
+        _need(page_table.dim() == 2, "page_table: [batch, max_pages]")
+        _ints("page_table", page_table, page_table.shape, dev)
+        _ints("len", length, (page_table.shape[0],), dev)
+        self.k_pages, self.v_pages, self.page_table, self.len = k_pages, v_pages, page_table, length
+        self.device = dev
+        n_pages, G, page, dh = k_pages.shape
+        self.s = hymba_paged_kv(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), length.data_ptr(),
+                                n_pages, page, page_table.shape[1], page_table.shape[0], G, dh, v_pages.shape[3], code)
+        self.ref = ctypes.byref(self.s)
+
+
+def attn_prefill_packed(shape, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                        o: torch.Tensor) -> None:
+    """o [rows, H * dv] = causal attention of the packed prompts q [rows, H * dh], k [rows,
+    G * dh], v [rows, G * dv]; cu_seqlens int32 [sequences + 1]."""
+    s, dev, rows = shape, q.device, q.shape[0]
+    lds = [_rows(n, t, w, s.dtype, dev) for n, t, w in (
+        ("q", q, s.n_q_heads * s.head_dim), ("k", k, s.n_kv_heads * s.head_dim), ("v", v, s.n_kv_heads * s.v_head_dim),
+        ("o", o, s.n_q_heads * s.v_head_dim))]
+    _need(k.shape[0] == rows and v.shape[0] == rows and o.shape[0] == rows, "q, k, v and o: as many rows")
+    _ints("cu_seqlens", cu_seqlens, (cu_seqlens.numel(),), dev)
+    _queue(dev, hymba_attn_prefill_packed, ctypes.byref(s), q.data_ptr(), lds[0], k.data_ptr(), lds[1], v.data_ptr(),
+           lds[2], cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, rows, o.data_ptr(), lds[3])
+
+
+def kv_append_paged(kv: PagedKV, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None) -> None:
+    """The rows of k [rows, G * dh] and v [rows, G * dv] become their sequences' newest
+    positions (kv.len counts them already); cu_seqlens None: one row per sequence."""
+    s, dev = kv.s, kv.device
+    ldk, ldv = _rows("k", k, s.n_kv_heads * s.head_dim, s.dtype, dev), _rows("v", v, s.n_kv_heads * s.v_head_dim, s.dtype, dev)
+    _need(k.shape[0] == v.shape[0], "k and v: as many rows")
+    if cu_seqlens is not None:
+        _ints("cu_seqlens", cu_seqlens, (s.batch + 1,), dev)
+    _queue(dev, hymba_kv_append_paged, kv.ref, k.data_ptr(), ldk, v.data_ptr(), ldv,
+           None if cu_seqlens is None else cu_seqlens.data_ptr(), k.shape[0])
+
+
+def decode_paged_workspace(shape, batch: int, max_len: int, device="cuda") -> torch.Tensor:
+    n = hymba_attn_decode_paged_workspace(ctypes.byref(shape), batch, max_len)
+    _need(n > 0, "invalid attention shape, batch or length")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def attn_decode_paged(shape, q: torch.Tensor, kv: PagedKV, o: torch.Tensor, ws: torch.Tensor, max_len: int = 0) -> None:
+    """o [batch, H * dv] = attention of the newest position of every sequence (q [batch, H *
+    dh]) over its pages. max_len: a bound on every length (0: the page table's capacity);
+    ws from decode_paged_workspace with that bound."""
+    s, dev = shape, kv.device
+    ldq, ldo = _rows("q", q, s.n_q_heads * s.head_dim, s.dtype, dev), _rows("o", o, s.n_q_heads * s.v_head_dim, s.dtype, dev)
+    _need(q.shape[0] == kv.s.batch and o.shape[0] == kv.s.batch, "q and o: one row per sequence")
+    _need(ws.device == dev and ws.is_contiguous(), "workspace: contiguous, on the cache's device")
+    _queue(dev, hymba_attn_decode_paged, ctypes.byref(s), q.data_ptr(), ldq, kv.ref, max_len, o.data_ptr(), ldo,
+           ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def _linear_rows(s, q, k, v, g, o, dev):
+    rows = q.shape[0]
+    lds = [_rows(n, t, w, s.dtype, dev) for n, t, w in (
+        ("q", q, s.n_qk_heads * s.key_dim), ("k", k, s.n_qk_heads * s.key_dim), ("v", v, s.n_heads * s.v_head_dim),
+        ("o", o, s.n_heads * s.v_head_dim))]
+    _need(k.shape[0] == rows and v.shape[0] == rows and o.shape[0] == rows, "q, k, v and o: as many rows")
+    if g.dim() == 1:
+        # one decay per head for every row
+        _floats("g", g, (s.n_heads,), dev)
+        return lds, 0
+    _need(g.shape[0] == rows, "g: [n_heads], or [rows, n_heads]")
+    if rows > 1 and g.stride(0) == 0:
+        _rows("g", g[:1], s.n_heads, HYMBA_F32, dev)
+        return lds, 0
+    return lds, _rows("g", g, s.n_heads, HYMBA_F32, dev)
+
+
+def linattn_workspace(shape, n_seqs: int, rows: int, device="cuda") -> torch.Tensor:
+    n = hymba_linattn_workspace(ctypes.byref(shape), n_seqs, rows)
+    _need(n > 0, "invalid linear-attention shape, sequence count or row count")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def linattn_prefill(shape, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor,
+                    o: torch.Tensor, ws: torch.Tensor, state_in: Optional[torch.Tensor] = None,
+                    state_out: Optional[torch.Tensor] = None) -> None:
+    """o [rows, H * dv] of the packed prompts q, k [rows, Hk * dk], v [rows, H * dv] with log
+    decays g float32 [rows, H] or [H]; states float32 [sequences, H, dv, dk] before and
+    after the prompts."""
+    s, dev = shape, q.device
+    lds, ldg = _linear_rows(s, q, k, v, g, o, dev)
+    _ints("cu_seqlens", cu_seqlens, (cu_seqlens.numel(),), dev)
+    n = cu_seqlens.numel() - 1
+    for name, t in (("state_in", state_in), ("state_out", state_out)):
+        if t is not None:
+            _floats(name, t, (n, s.n_heads, s.v_head_dim, s.key_dim), dev)
+    _need(ws.device == dev and ws.is_contiguous(), "workspace: contiguous, on the rows' device")
+    _queue(dev, hymba_linattn_prefill, ctypes.byref(s), q.data_ptr(), lds[0], k.data_ptr(), lds[1], v.data_ptr(),
+           lds[2], g.data_ptr(), ldg, cu_seqlens.data_ptr(), n, q.shape[0],
+           None if state_in is None else state_in.data_ptr(), None if state_out is None else state_out.data_ptr(),
+           o.data_ptr(), lds[3], ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def linattn_step(shape, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
+                 o: torch.Tensor) -> None:
+    """One token per sequence: state float32 [batch, H, dv, dk] is updated in place, o [batch,
+    H * dv] is its product with the token's query."""
+    s, dev = shape, q.device
+    lds, ldg = _linear_rows(s, q, k, v, g, o, dev)
+    _floats("state", state, (q.shape[0], s.n_heads, s.v_head_dim, s.key_dim), dev)
+    _queue(dev, hymba_linattn_step, ctypes.byref(s), q.data_ptr(), lds[0], k.data_ptr(), lds[1], v.data_ptr(), lds[2],
+           g.data_ptr(), ldg, state.data_ptr(), q.shape[0], o.data_ptr(), lds[3])

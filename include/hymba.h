@@ -306,6 +306,144 @@ uint64_t hymba_ssm_state_bytes(int n_layers, int channels, int d_state, int batc
 int hymba_attn_decode_static(const hymba_layer_cfg* cfg, const void* q, int64_t ldq, const hymba_kv* kv,
                              void* o, int B, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Ragged batches: sequences of different lengths in one call. The mixer calls above take
+ * rectangular batches and one contiguous cache per sequence; the entry points below
+ * run the mixing steps of the two head families on their own, as
+ * hymba_attn_decode_static does, for callers that pack prompts of different lengths
+ * into one buffer of rows and keep K and V in pages.
+ *
+ * Rows: q, k, v and o are rows of `ld` elements (ldq, ldk, ldv, ldo) whose heads lie side
+ * by side from the row's start, so the columns of a fused projection are passed by
+ * pointing at the first one. Base pointers and row strides must be multiples of 16 bytes
+ * (HYMBA_ERR_INVALID_ARG otherwise), and a stride no shorter than its row. o must not
+ * overlap the elements of q, k and v. Sequence s of a packed batch owns the rows
+ * cu_seqlens[s] .. cu_seqlens[s+1] - 1 (device, int32, n_seqs + 1 entries, not
+ * descending, within 0 .. total_rows; empty sequences are allowed). Rows that belong to
+ * no sequence are neither used nor written. A sequence whose offsets break that rule is
+ * left out (its rows are not written, its state neither) and HYMBA_ERR_DEVICE_RANGE is
+ * recorded in the status word.
+ *
+ * Element types: HYMBA_F16 (the type of K and V inside a bf16 layer), HYMBA_BF16 and
+ * HYMBA_F32. Products of 16-bit operands run on the tensor cores with fp32
+ * accumulation, fp32 ones on the CUDA cores; softmax statistics and states are fp32.
+ * Values at places that a row does not see, non-finite ones among them, do not reach
+ * the row's output. All calls only queue work on `stream`: they can be captured into a
+ * graph, and calls on different streams may overlap as long as they share no output and
+ * no workspace.
+ * --------------------------------------------------------------------------- */
+
+/* Attention heads of a ragged batch. head_dim and v_head_dim 64 or 128 each; n_q_heads a
+ * multiple of n_kv_heads, at most 1024 (HYMBA_ERR_UNSUPPORTED otherwise). Visibility as in
+ * a layer, counted from the sequence's first row: key j is visible to query i iff j <= i
+ * and (j < n_meta or i - j < window); window <= 0 means global. */
+typedef struct hymba_attn_shape {
+    int32_t n_q_heads;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t v_head_dim;
+    int32_t n_meta;
+    int32_t window;
+    int32_t dtype;  /* of q, k, v and o: HYMBA_F16, HYMBA_BF16 or HYMBA_F32 */
+    float   scale;  /* of the scores; 0: 1 / sqrt(head_dim) */
+} hymba_attn_shape;
+
+/* Causal attention over whole prompts packed back to back: o_i = sum_j p_ij v_j / sum_j
+ * p_ij with p_ij = exp(scale q_i . k_j) over the keys j that row i of the same sequence
+ * sees. q [total_rows, n_q_heads * head_dim], k [total_rows, n_kv_heads * head_dim],
+ * v [total_rows, n_kv_heads * v_head_dim], o [total_rows, n_q_heads * v_head_dim] (after
+ * RoPE, where the layer has it). total_rows may be 0 (no work), at most 2^30. A row
+ * whose visible scores are all -infinity returns zeros. */
+int hymba_attn_prefill_packed(const hymba_attn_shape* shape, const void* q, int64_t ldq, const void* k,
+                              int64_t ldk, const void* v, int64_t ldv, const int32_t* cu_seqlens, int n_seqs,
+                              int total_rows, void* o, int64_t ldo, void* stream);
+
+/* K and V of a batch of sequences in pages of page_size positions (any size >= 1):
+ * k_pages [n_pages, n_kv_heads, page_size, head_dim], v_pages [n_pages, n_kv_heads,
+ * page_size, v_head_dim]. Position p of sequence b is slot p mod page_size of page
+ * page_table[b, p / page_size] (page_table [batch, max_pages]). len[b] = positions the
+ * sequence holds, 0 .. max_pages * page_size (which must not pass 2^30). All arrays are
+ * device memory of the caller, the pages 16-byte aligned. Sequences may share pages they
+ * only read. Table entries of pages that hold no position a call touches are not
+ * read, so a windowed layer's old pages can be given back. */
+typedef struct hymba_paged_kv {
+    void*          k_pages;
+    void*          v_pages;
+    const int32_t* page_table;
+    const int32_t* len;
+    int32_t        n_pages;
+    int32_t        page_size;
+    int32_t        max_pages;
+    int32_t        batch;
+    int32_t        n_kv_heads;
+    int32_t        head_dim;
+    int32_t        v_head_dim;
+    int32_t        dtype;
+} hymba_paged_kv;
+
+/* Write new rows into the pages. Sequence b's n_b = cu_seqlens[b+1] - cu_seqlens[b] rows of
+ * k [total_rows, n_kv_heads * head_dim] and v [total_rows, n_kv_heads * v_head_dim] become
+ * its newest positions len[b] - n_b .. len[b] - 1: len already counts them (the caller
+ * advances it, on the same stream, before the call). cu_seqlens NULL: one row per
+ * sequence, total_rows = batch. A row whose position or page is out of range is not
+ * written and HYMBA_ERR_DEVICE_RANGE is recorded. Rows of two sequences that meet in one
+ * slot race: one of them stays. */
+int hymba_kv_append_paged(const hymba_paged_kv* kv, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                          const int32_t* cu_seqlens, int total_rows, void* stream);
+
+/* Attention of one new token per sequence over the pages: row b of q [batch, n_q_heads *
+ * head_dim] is position len[b] - 1, whose K and V are already in the cache. o [batch,
+ * n_q_heads * v_head_dim]. A sequence of length 0 returns zeros; one that is longer than
+ * max_len (the host's bound on every len[b], at most max_pages * page_size; 0 means that
+ * product), has a negative length or needs a page outside 0 .. n_pages - 1 returns
+ * zeros and records HYMBA_ERR_DEVICE_RANGE. The shape's heads, dims and dtype must be
+ * the cache's (HYMBA_ERR_KV_INCOMPATIBLE). The keys are split over blocks by max_len and
+ * the batch; the partial results meet in `workspace` (256-byte aligned, at least
+ * hymba_attn_decode_paged_workspace(shape, batch, max_len) bytes with the same max_len
+ * as the call, or its page capacity where the call passes 0; contents are undefined
+ * before and after; calls that may overlap need workspaces of their own). */
+int hymba_attn_decode_paged(const hymba_attn_shape* shape, const void* q, int64_t ldq, const hymba_paged_kv* kv,
+                            int max_len, void* o, int64_t ldo, void* workspace, size_t ws_bytes, void* stream);
+/* Bytes of that workspace (0 if an argument is invalid). */
+size_t hymba_attn_decode_paged_workspace(const hymba_attn_shape* shape, int batch, int max_len);
+
+/* Linear attention with a decay for each head, the recurrence of the SSD form ("Lecture
+ * 04 - Beyond the Dense Transformer", section 3) with keys and queries in the place of B
+ * and C: S_t = exp(g_t) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t per head, g_t the head's
+ * log decay at row t (normally <= 0; -infinity forgets everything before the row).
+ * n_qk_heads divides n_heads (at most 1024): head h reads q and k of head h / (n_heads /
+ * n_qk_heads); the SSD form's shared B and C are n_qk_heads = 1. key_dim 16, 64 or 128;
+ * v_head_dim a multiple of 64, at most 512 (HYMBA_ERR_UNSUPPORTED otherwise). States are
+ * fp32 [n, n_heads, v_head_dim, key_dim], the layout of hymba_ssm_state.h. */
+typedef struct hymba_linattn_shape {
+    int32_t n_qk_heads;
+    int32_t n_heads;
+    int32_t key_dim;
+    int32_t v_head_dim;
+    int32_t dtype;  /* of q, k, v and o: HYMBA_F16, HYMBA_BF16 or HYMBA_F32 */
+    float   scale;  /* of the output; 0: 1 / sqrt(key_dim) */
+} hymba_linattn_shape;
+
+/* Whole prompts, packed. q, k [total_rows, n_qk_heads * key_dim], v and o [total_rows,
+ * n_heads * v_head_dim]; g fp32 [total_rows, n_heads] with row stride ldg elements (0: one
+ * row of decays for all rows). state_in: the state before each sequence's first row
+ * (NULL: zero); state_out: the state after its last (NULL: not kept; may equal
+ * state_in, and may not overlap it otherwise). An empty sequence's state_out is its
+ * state_in. Workspace: hymba_linattn_workspace bytes, 256-byte aligned, contents undefined
+ * before and after; calls that may overlap need workspaces of their own. */
+int hymba_linattn_prefill(const hymba_linattn_shape* shape, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                          const void* v, int64_t ldv, const float* g, int64_t ldg, const int32_t* cu_seqlens,
+                          int n_seqs, int total_rows, const float* state_in, float* state_out, void* o, int64_t ldo,
+                          void* workspace, size_t ws_bytes, void* stream);
+/* Bytes of that workspace (0 if an argument is invalid). */
+size_t hymba_linattn_workspace(const hymba_linattn_shape* shape, int n_seqs, int total_rows);
+
+/* One token per sequence: row b of q, k, v, g and o belongs to state[b], which is updated in
+ * place. ldg as above. */
+int hymba_linattn_step(const hymba_linattn_shape* shape, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                       const void* v, int64_t ldv, const float* g, int64_t ldg, float* state, int batch, void* o,
+                       int64_t ldo, void* stream);
+
 /* Synchronises `stream`, then returns and clears the status word of the current
  * device: HYMBA_OK, HYMBA_ERR_DEVICE_TIMEOUT or HYMBA_ERR_DEVICE_RANGE; or
  * HYMBA_ERR_CUDA if the synchronisation itself failed. */
