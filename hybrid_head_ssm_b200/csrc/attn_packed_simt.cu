@@ -196,7 +196,5 @@ int launch_attn_packed_simt(const Ctx& ctx, const PackedAttn& a) {
 }
 
 template int launch_attn_packed_simt<float>(const Ctx&, const PackedAttn&);
-template int launch_attn_packed_simt<f16>(const Ctx&, const PackedAttn&);
-template int launch_attn_packed_simt<bf16>(const Ctx&, const PackedAttn&);
 
 }  // namespace hymba

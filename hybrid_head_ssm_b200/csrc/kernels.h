@@ -143,6 +143,9 @@ struct PackedAttn {
 // CUDA cores (fp32 rows)
 template <typename T>
 int launch_attn_packed_simt(const Ctx& ctx, const PackedAttn& a);
+// tcgen05 tensor cores (fp16 or bf16 rows)
+template <typename T>
+int launch_attn_packed_tc(const Ctx& ctx, const PackedAttn& a);
 
 // New rows into pages (elements of esz bytes); cu NULL: one row per sequence.
 int launch_kv_append(const Ctx& ctx, const hymba_paged_kv& kv, int esz, const void* k, long long ldk, const void* v,

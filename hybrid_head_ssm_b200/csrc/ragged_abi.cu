@@ -80,8 +80,8 @@ int hymba_attn_prefill_packed(const hymba_attn_shape* shape, const void* q, int6
     a.n_meta = s.n_meta; a.window = s.window;
     a.scale = attn_scale(shape);
     if (s.dtype == HYMBA_F32) return launch_attn_packed_simt<float>(ctx, a);
-    if (s.dtype == HYMBA_F16) return launch_attn_packed_simt<f16>(ctx, a);
-    return launch_attn_packed_simt<bf16>(ctx, a);
+    if (s.dtype == HYMBA_F16) return launch_attn_packed_tc<f16>(ctx, a);
+    return launch_attn_packed_tc<bf16>(ctx, a);
 }
 
 int hymba_kv_append_paged(const hymba_paged_kv* kv, const void* k, int64_t ldk, const void* v, int64_t ldv,
