@@ -239,6 +239,250 @@ __global__ void __launch_bounds__(128) decode_paged_simt_kernel(const DecodeArgs
     }
 }
 
+// Tensor cores (16-bit rows): one block of 4 warps per (key split, KV head and group of up
+// to 8 NG of its query heads, sequence). Each warp walks every fourth 16-key tile of the split
+// with its own ring of cp.async stages and its own running max, so no warp waits for
+// another until the split ends; 96 KB of ring per block keeps two blocks per SM and about
+// 150 KB per SM in flight. Per tile: S^T = K q^T (keys x heads, K by ldmatrix, q as the B
+// operand in registers), p = 2^(s - m) with O rescaled only when a max grows by more than
+// 2^8, and O^T += V^T P^T (V^T by transposing ldmatrix, P^T by an 8 x 8 register transpose).
+// p enters the product as two 16-bit parts (p = hi + lo), so the weights keep 16 bits or
+// more. Slots are looked up one tile ahead of their copies: lane i holds key i's row. Rows
+// past the split's last key are zero-filled by the copy and masked. Bound by HBM: K and V
+// of every visible key once.
+constexpr int TK = 16;                 // keys per tile
+constexpr int RING = 24 * 1024;        // bytes of one warp's ring
+template <int DH, int DV>
+struct Ring {
+    static constexpr int KB = TK * DH * 2, VB = TK * DV * 2, BYTES = KB + VB, N = RING / BYTES;
+};
+
+template <typename T, int DH, int DV, int NG>
+__global__ void __launch_bounds__(128, 2) decode_paged_mma_kernel(const DecodeArgs<T> a, int* status) {
+    using R_ = Ring<DH, DV>;
+    griddep_sync();
+    extern __shared__ __align__(128) uint8_t decode_raw[];
+    __shared__ float ms[4][8 * NG], ls[4][8 * NG];
+    const int R = a.H / a.G, groups = (R + 8 * NG - 1) / (8 * NG);
+    const int split = blockIdx.x, g = blockIdx.y / groups, grp = blockIdx.y % groups, b = blockIdx.z;
+    const int h0 = g * R + grp * 8 * NG, nh = min(8 * NG, R - grp * 8 * NG);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int lg = lane >> 2, lq = lane & 3;
+    View w;
+    const bool fine = view_of(a, b, &w);
+    if (!fine && split == 0 && blockIdx.y == 0 && tid == 0) set_status(status, HYMBA_ERR_DEVICE_RANGE);
+    const int k0 = split * a.split_keys, k1 = min(w.n, k0 + a.split_keys);
+    if (k0 >= k1 && split > 0) return;
+    const int ntile = k1 > k0 ? (k1 - k0 + TK - 1) / TK : 0;
+    uint8_t* ring = decode_raw + warp * RING;
+
+    // q as the "col" operand: heads x dims
+    uint32_t qf[NG][DH / 16][2];
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk) {
+            const int h = n * 8 + lg;
+            const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q + b * a.ldq + (long long)(h0 + min(h, nh - 1)) * DH +
+                                                                   kk * 16 + 2 * lq);
+            qf[n][kk][0] = h < nh ? qp[0] : 0u;
+            qf[n][kk][1] = h < nh ? qp[4] : 0u;
+        }
+    float ot[NG][DV / 16][4];
+    float m[NG][2], l[NG][2];
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+        for (int t = 0; t < DV / 16; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ot[n][t][e] = 0.f;
+    }
+
+    // the row (head g) of key `lane % 16` of the warp's i-th tile; none past the end
+    constexpr uint32_t NONE = 0xffffffffu;
+    int bad = 0;
+    auto row_of = [&](int i) -> uint32_t {
+        const int j = k0 + (warp + 4 * i) * TK + (lane & 15);
+        if (j >= k1) return NONE;
+        const long long s = slot_of(a, b, w.pos(j));
+        if (s < 0) {
+            bad = 1;
+            return NONE;
+        }
+        return (uint32_t)(s + (long long)g * a.page);
+    };
+    const int mine = ntile > warp ? (ntile - warp + 3) / 4 : 0;  // the warp's tiles
+    auto issue = [&](int i, uint32_t row) {
+        uint8_t* st = ring + (i % R_::N) * R_::BYTES;
+        constexpr int KC = DH / 8, VC = DV / 8;  // 16-byte pieces per row
+#pragma unroll
+        for (int x = 0; x < TK * KC / 32; ++x) {
+            const int r = x * (32 / KC) + lane / KC, c = lane % KC;
+            const uint32_t rr = __shfl_sync(0xffffffffu, row, r);
+            wm::cpa16(st + r * DH * 2 + ((c ^ (r & 7)) * 16), a.k_pages + (rr == NONE ? 0 : (long long)rr * DH) + c * 8,
+                      rr == NONE);
+        }
+#pragma unroll
+        for (int x = 0; x < TK * VC / 32; ++x) {
+            const int r = x * (32 / VC) + lane / VC, c = lane % VC;
+            const uint32_t rr = __shfl_sync(0xffffffffu, row, r);
+            wm::cpa16(st + R_::KB + r * DV * 2 + ((c ^ (r & 7)) * 16),
+                      a.v_pages + (rr == NONE ? 0 : (long long)rr * DV) + c * 8, rr == NONE);
+        }
+    };
+    {
+        uint32_t row[R_::N - 1];
+#pragma unroll
+        for (int i = 0; i < R_::N - 1; ++i) row[i] = i < mine ? row_of(i) : NONE;
+#pragma unroll
+        for (int i = 0; i < R_::N - 1; ++i) {
+            if (i < mine) issue(i, row[i]);
+            wm::cpa_commit();
+        }
+    }
+    uint32_t next = R_::N - 1 < mine ? row_of(R_::N - 1) : NONE;
+    for (int i = 0; i < mine; ++i) {
+        wm::cpa_wait<R_::N - 2>();
+        __syncwarp();  // every lane's copies of the tile are there, and its reads of the stage that is filled next are done
+        if (i + R_::N - 1 < mine) issue(i + R_::N - 1, next);
+        wm::cpa_commit();
+        if (i + R_::N < mine) next = row_of(i + R_::N);
+        const uint8_t* st = ring + (i % R_::N) * R_::BYTES;
+        float sc[NG][4];
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk) {
+            uint32_t kf[4];
+            const int r = lane & 15, c = 2 * kk + (lane >> 4);
+            wm::ldsm_x4(kf, st + r * DH * 2 + ((c ^ (r & 7)) * 16));
+#pragma unroll
+            for (int n = 0; n < NG; ++n) wm::mma16<T>(sc[n], kf, qf[n][kk][0], qf[n][kk][1]);
+        }
+        // keys lg and lg + 8 of the tile, heads 2 lq and 2 lq + 1
+        const int left = k1 - (k0 + (warp + 4 * i) * TK);
+        uint32_t ph[NG][2], pl[NG][2];
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            if (left < TK) {
+                if (lg >= left) sc[n][0] = sc[n][1] = -INFINITY;
+                if (lg + 8 >= left) sc[n][2] = sc[n][3] = -INFINITY;
+            }
+            float mx[2] = {fmaxf(sc[n][0], sc[n][2]), fmaxf(sc[n][1], sc[n][3])};
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
+                mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
+            }
+            mx[0] *= a.scale_log2;
+            mx[1] *= a.scale_log2;
+            if (__any_sync(0xffffffffu, mx[0] > m[n][0] + 8.f || mx[1] > m[n][1] + 8.f)) {
+                float f[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float to = fmaxf(m[n][e], mx[e]);
+                    f[e] = to == -INFINITY ? 1.f : fast_exp2(m[n][e] - to);
+                    m[n][e] = to;
+                    l[n][e] *= f[e];
+                }
+#pragma unroll
+                for (int t = 0; t < DV / 16; ++t) {
+                    ot[n][t][0] *= f[0];
+                    ot[n][t][1] *= f[1];
+                    ot[n][t][2] *= f[0];
+                    ot[n][t][3] *= f[1];
+                }
+            }
+            const float u0 = m[n][0] == -INFINITY ? 0.f : m[n][0], u1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+            const float p0 = fast_exp2(fmaf(sc[n][0], a.scale_log2, -u0)), p1 = fast_exp2(fmaf(sc[n][1], a.scale_log2, -u1));
+            const float p2 = fast_exp2(fmaf(sc[n][2], a.scale_log2, -u0)), p3 = fast_exp2(fmaf(sc[n][3], a.scale_log2, -u1));
+            l[n][0] += p0 + p2;
+            l[n][1] += p1 + p3;
+            uint32_t h01, l01, h23, l23;
+            wm::split2<T>(p0, p1, &h01, &l01);
+            wm::split2<T>(p2, p3, &h23, &l23);
+            ph[n][0] = wm::transpose8(h01);
+            ph[n][1] = wm::transpose8(h23);
+            pl[n][0] = wm::transpose8(l01);
+            pl[n][1] = wm::transpose8(l23);
+        }
+#pragma unroll
+        for (int t = 0; t < DV / 16; ++t) {
+            uint32_t vf[4];
+            const int r = (lane & 7) + 8 * (lane >> 4), c = 2 * t + ((lane >> 3) & 1);
+            wm::ldsm_x4_t(vf, st + R_::KB + r * DV * 2 + ((c ^ (r & 7)) * 16));
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                wm::mma16<T>(ot[n][t], vf, ph[n][0], ph[n][1]);
+                wm::mma16<T>(ot[n][t], vf, pl[n][0], pl[n][1]);
+            }
+        }
+    }
+    wm::cpa_wait<0>();
+    // join the warps: one max per head, each warp's sums brought to it
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
+            if (lg == 0) {
+                ms[warp][n * 8 + 2 * lq + e] = m[n][e];
+                ls[warp][n * 8 + 2 * lq + e] = l[n][e];
+            }
+        }
+    bad = __syncthreads_or(bad);
+    if (bad && tid == 0) set_status(status, HYMBA_ERR_DEVICE_RANGE);
+    constexpr int LD = DV + 4;
+    float* acc = reinterpret_cast<float*>(decode_raw);  // [4][8 NG][LD]
+    static_assert(4 * 8 * NG * LD * 4 <= 4 * RING, "the joined sums reuse the rings");
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int h = n * 8 + 2 * lq + e;
+            const float to = fmaxf(fmaxf(ms[0][h], ms[1][h]), fmaxf(ms[2][h], ms[3][h]));
+            f[e] = m[n][e] == -INFINITY ? 0.f : fast_exp2(m[n][e] - to);
+            // (a NaN or infinite max keeps a NaN sum)
+            if (!(l[n][e] == l[n][e])) f[e] = l[n][e];
+        }
+#pragma unroll
+        for (int t = 0; t < DV / 16; ++t) {
+            float* p = acc + (warp * 8 * NG + n * 8 + 2 * lq) * LD + 16 * t + lg;
+            p[0] = ot[n][t][0] * f[0];
+            p[LD] = ot[n][t][1] * f[1];
+            p[8] = ot[n][t][2] * f[0];
+            p[LD + 8] = ot[n][t][3] * f[1];
+        }
+    }
+    __syncthreads();
+    for (int x = tid; x < nh * DV; x += 128) {
+        const int h = x / DV, col = x % DV;
+        float to = fmaxf(fmaxf(ms[0][h], ms[1][h]), fmaxf(ms[2][h], ms[3][h]));
+        float sum = 0.f, lt = 0.f;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            sum += acc[(v * 8 * NG + h) * LD + col];
+            lt += ms[v][h] == -INFINITY ? ls[v][h] : ls[v][h] * fast_exp2(ms[v][h] - to);
+        }
+        if (a.n_split == 1) {
+            a.o[b * a.ldo + (long long)(h0 + h) * DV + col] = from_f<T>(bad || lt == 0.f ? 0.f : sum / lt);
+        } else {
+            float* p = a.part + (((long long)b * a.H + h0 + h) * a.n_split + split) * (DV + 4);
+            p[col] = sum;
+            if (col == 0) {
+                p[DV] = to;
+                p[DV + 1] = bad ? -1.f : lt;
+            }
+        }
+    }
+}
+
 // Join the key splits of one (query head, sequence): weights 2^(m_s - max m).
 template <typename T, int DV>
 __global__ void __launch_bounds__(DV) decode_paged_join_kernel(const DecodeArgs<T> a) {
@@ -268,10 +512,13 @@ __global__ void __launch_bounds__(DV) decode_paged_join_kernel(const DecodeArgs<
 struct Split {
     int keys, n;
 };
+int heads_per_block(const hymba_attn_shape& s) {
+    return s.dtype == HYMBA_F32 || s.n_q_heads / s.n_kv_heads <= 8 ? 8 : 16;
+}
 Split split_of(const hymba_attn_shape& s, int batch, int max_len) {
     const long long span = s.window > 0 ? std::min<long long>(max_len, (long long)s.n_meta + s.window) : max_len;
-    const int R = s.n_q_heads / s.n_kv_heads;
-    const long long units = (long long)batch * s.n_kv_heads * ((R + SR - 1) / SR);
+    const int R = s.n_q_heads / s.n_kv_heads, hb = heads_per_block(s);
+    const long long units = (long long)batch * s.n_kv_heads * ((R + hb - 1) / hb);
     const long long chunks = (span + SC - 1) / SC;
     const long long want = std::max<long long>(1, std::min(chunks, (148 * 8 + units - 1) / units));
     Split r;
@@ -280,11 +527,28 @@ Split split_of(const hymba_attn_shape& s, int batch, int max_len) {
     return r;
 }
 
-template <typename T, int DH, int DV>
-int launch_decode_dims(const Ctx& ctx, DecodeArgs<T> a, int batch) {
+template <typename T, int DH, int DV, int NG>
+int launch_decode_mma(const Ctx& ctx, const DecodeArgs<T>& a, int batch) {
     const int R = a.H / a.G;
-    dim3 grid(a.n_split, a.G * ((R + SR - 1) / SR), batch);
-    HYMBA_LAUNCH(ctx, "attn_decode_paged", (decode_paged_simt_kernel<T, DH, DV>), grid, 128, 0, a, ctx.status);
+    auto kern = decode_paged_mma_kernel<T, DH, DV, NG>;
+    const size_t smem = 4 * RING;
+    static std::atomic<unsigned long long> smem_set{0};
+    if (!smem_opt_in_once(smem_set, kern, smem, ctx)) return HYMBA_ERR_CUDA;
+    dim3 grid(a.n_split, a.G * ((R + 8 * NG - 1) / (8 * NG)), batch);
+    HYMBA_LAUNCH(ctx, "attn_decode_paged", kern, grid, 128, smem, a, ctx.status);
+    return HYMBA_OK;
+}
+
+template <typename T, int DH, int DV>
+int launch_decode_dims(const Ctx& ctx, const DecodeArgs<T>& a, int batch) {
+    const int R = a.H / a.G;
+    if constexpr (sizeof(T) == 2) {
+        const int rc = R <= 8 ? launch_decode_mma<T, DH, DV, 1>(ctx, a, batch) : launch_decode_mma<T, DH, DV, 2>(ctx, a, batch);
+        if (rc) return rc;
+    } else {
+        dim3 grid(a.n_split, a.G * ((R + SR - 1) / SR), batch);
+        HYMBA_LAUNCH(ctx, "attn_decode_paged", (decode_paged_simt_kernel<T, DH, DV>), grid, 128, 0, a, ctx.status);
+    }
     if (a.n_split > 1)
         HYMBA_LAUNCH(ctx, "attn_decode_paged_join", (decode_paged_join_kernel<T, DV>), dim3(a.H, batch), DV, 0, a);
     return HYMBA_OK;

@@ -46,7 +46,8 @@ int check_paged(const hymba_paged_kv* kv) {
         (((uintptr_t)kv->page_table | (uintptr_t)kv->len) & 3))
         return HYMBA_ERR_INVALID_ARG;
     if (!dim_ok(kv->head_dim) || !dim_ok(kv->v_head_dim) || kv->n_kv_heads > 1024 ||
-        (int64_t)kv->max_pages * kv->page_size > kMostRows || kv->batch > 65535)
+        (int64_t)kv->max_pages * kv->page_size > kMostRows || kv->batch > 65535 ||
+        (int64_t)kv->n_pages * kv->page_size > 0x7fffffffLL / kv->n_kv_heads)
         return HYMBA_ERR_UNSUPPORTED;
     return HYMBA_OK;
 }

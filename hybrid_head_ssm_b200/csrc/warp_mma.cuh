@@ -1,6 +1,8 @@
 // Warp-level tensor-core helpers: per-thread asynchronous copies into shared memory,
-// ldmatrix fragment loads and the m16n8k16 fp16 MMA with fp32 accumulators.
+// ldmatrix fragment loads and the m16n8k16 fp16 and bf16 MMAs with fp32 accumulators.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace hymba {
@@ -40,6 +42,34 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// either 16-bit type
+template <typename T>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<T, bf16>::value) mma_bf16(c, a[0], a[1], a[2], a[3], b0, b1);
+    else mma_f16(c, a[0], a[1], a[2], a[3], b0, b1);
+}
+// x = hi + lo, both packed pairs of T: about twice T's mantissa bits
+template <typename T>
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t* hi, uint32_t* lo) {
+    *hi = pack2<T>(x0, x1);
+    const T* h = reinterpret_cast<const T*>(hi);
+    *lo = pack2<T>(x0 - to_f(h[0]), x1 - to_f(h[1]));
+}
+// transpose of an 8 x 8 matrix of 16-bit elements held one row per four lanes
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <int N>
+__device__ __forceinline__ void cpa_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);

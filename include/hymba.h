@@ -362,8 +362,9 @@ int hymba_attn_prefill_packed(const hymba_attn_shape* shape, const void* q, int6
  * k_pages [n_pages, n_kv_heads, page_size, head_dim], v_pages [n_pages, n_kv_heads,
  * page_size, v_head_dim]. Position p of sequence b is slot p mod page_size of page
  * page_table[b, p / page_size] (page_table [batch, max_pages]). len[b] = positions the
- * sequence holds, 0 .. max_pages * page_size (which must not pass 2^30). All arrays are
- * device memory of the caller, the pages 16-byte aligned. Sequences may share pages they
+ * sequence holds, 0 .. max_pages * page_size (which must not pass 2^30). n_pages *
+ * n_kv_heads * page_size must stay below 2^31, batch below 2^16. All arrays are device
+ * memory of the caller, the pages 16-byte aligned. Sequences may share pages they
  * only read. Table entries of pages that hold no position a call touches are not
  * read, so a windowed layer's old pages can be given back. */
 typedef struct hymba_paged_kv {
