@@ -171,5 +171,8 @@ struct LinAttn {
 };
 template <typename T>
 int launch_linattn_recurrent(const Ctx& ctx, const LinAttn& a);
+// Packed prompts of 16-bit rows in chunks of 64 rows, tensor cores.
+template <typename T>
+int launch_linattn_chunk(const Ctx& ctx, const LinAttn& a);
 
 }  // namespace hymba

@@ -177,8 +177,8 @@ int hymba_linattn_prefill(const hymba_linattn_shape* shape, const void* q, int64
     a.n_seqs = n_seqs;
     a.total = total_rows;
     if (shape->dtype == HYMBA_F32) return launch_linattn_recurrent<float>(ctx, a);
-    if (shape->dtype == HYMBA_F16) return launch_linattn_recurrent<f16>(ctx, a);
-    return launch_linattn_recurrent<bf16>(ctx, a);
+    if (shape->dtype == HYMBA_F16) return launch_linattn_chunk<f16>(ctx, a);
+    return launch_linattn_chunk<bf16>(ctx, a);
 }
 
 int hymba_linattn_step(const hymba_linattn_shape* shape, const void* q, int64_t ldq, const void* k, int64_t ldk,
