@@ -15,16 +15,20 @@
 // form exp(cs_i) S q; then each adds P V for its columns and updates its S. The V fragments
 // serve as the B operand of P V and as the A operand of the update.
 //
-// Numbers: cs is summed in 64 bits and kept as hi + lo pairs, so a decay between two rows is
-// right to fp32 after any other row (one that forgets everything included). P and the copy of
-// S that meets q are rounded to the rows' type, like any MMA operand; the scaled v of the state
-// update enters as two 16-bit parts, so the fp32 state keeps 16 bits or more of every term.
-// fp16 has little range: P's rows, S's copy and the scaled v are brought to the middle of it by
-// powers of two, which are taken out again from the fp32 sums.
-// A row's values reach only what sees them: rows behind the sequence are zero-filled, a
-// decay of 0 drops what it multiplies, and a chunk whose V holds a value that is not finite
-// forms P V row by row.
-// Bound: HBM (q, k, v once per 64 value columns, o) with the MMAs close behind.
+// Numbers: cs is summed in 64 bits. A decay between rows j <= i is 2^(a_i + b_j) with a_i and b_j
+// the fp32 distances of cs_i and cs_j from the cs at the start of i's 16 rows, so it is right
+// to fp32 after any other row (one that forgets everything included) and never formed from two
+// factors. P and the copy of S that meets q are rounded to the rows' type, like any MMA operand;
+// the scaled v of the state update enters as two 16-bit parts, so the fp32 state keeps 16 bits
+// or more of every term. fp16 has
+// little range: P's rows, S's copy and v are brought to the middle of it by powers of two,
+// which are taken out again from the fp32 sums.
+// A row's values reach only what sees them: rows behind the sequence are zero-filled; in a
+// chunk where a decay may underflow to 0, what it multiplies is dropped; a chunk whose V holds a
+// value that is not finite forms P V row by row.
+// Bound: HBM (q, k, v once per 64 value columns, o) and the warp MMAs (1024 multiply-adds per
+// clock and SM measured) are close; what is left is instruction issue, hence the tables that
+// one warp (the one with the fewest tiles of P) forms a chunk ahead for all.
 #include "kernels.h"
 #include "ragged.cuh"
 
@@ -35,7 +39,17 @@ namespace {
 constexpr int CQ = 64;   // rows per chunk
 constexpr int CV = 64;   // value columns per CTA
 constexpr int NT = 128;  // 4 warps
-constexpr double LOG2E = 1.4426950408889634;
+
+// Per chunk, from its 64 log decays (log2 units; cs_i the inclusive sums):
+struct Tables {
+    alignas(16) float a[CQ];      // cs_i - cs at the start of i's 16 rows + log2 scale
+    alignas(16) float b[4][CQ];   // cs at the start of 16-row block t - cs_j, for j < 16 (t + 1)
+    alignas(16) float e[CQ];      // 2^cs_i scale
+    alignas(16) float w[CQ];      // 2^(cs_63 - cs_j)
+    float dec;                    // 2^cs_63
+    int resets;                   // a decay within the chunk may be 0
+    int grows;                    // a log decay is positive
+};
 
 template <int DK>
 struct ChunkSmem {
@@ -44,8 +58,8 @@ struct ChunkSmem {
     alignas(128) uint8_t k[2][CQ * DK * 2];
     alignas(128) uint8_t v[2][CQ * CV * 2];
     alignas(128) uint8_t p[CQ * CQ * 2];
-    alignas(16) float2 cs[4][CQ];  // each warp's copy: cs in log2 units, hi and lo
-    alignas(16) float ps[CQ];      // 1 / power of two that P's rows carry
+    Tables tab[2];
+    alignas(16) float ps[CQ];  // the power of two that P's rows carry
 };
 
 // byte offset of 16-byte piece c of row r of a tile of COLS 16-bit columns; 8 rows at one c
@@ -56,33 +70,128 @@ __device__ __forceinline__ uint32_t at(int r, int c) {
     else return r * COLS * 2 + ((c ^ (r & 7)) * 16);
 }
 
-// rows t0 .. t0 + 63 of the sequence; rows past its end read as zero
+// A thread's share of staging 64 rows of COLS columns: one 16-byte column piece of every
+// STEP-th row, so that its swizzle is one constant.
 template <typename T, int COLS>
-__device__ __forceinline__ void stage(uint8_t* dst, const T* src, long long ld, int t0, int len) {
-    constexpr int PC = COLS / 8;
-#pragma unroll
-    for (int x = threadIdx.x; x < CQ * PC; x += NT) {
-        const int r = x / PC, c = x % PC;
-        const bool in = t0 + r < len;
-        wm::cpa16(dst + at<COLS>(r, c), src + (in ? (long long)(t0 + r) * ld : 0) + c * 8, !in);
+struct Stager {
+    static constexpr int PC = COLS / 8, STEP = NT / PC < CQ ? NT / PC : CQ, N = CQ / STEP;
+    const char* src;  // the thread's first row of the next chunk
+    long long step;   // bytes between its rows
+    uint32_t dst;
+    int row;
+    bool on;
+    __device__ void init(const T* base, long long ld) {
+        row = threadIdx.x / PC;
+        on = row < CQ;
+        const int c = threadIdx.x % PC;
+        src = reinterpret_cast<const char*>(base + row * ld + c * 8);
+        step = ld * STEP * (long long)sizeof(T);
+        dst = at<COLS>(row, c);
     }
-}
+    // rows t0 .. t0 + 63; rows past the sequence's end read as zero
+    __device__ __forceinline__ void load(uint8_t* tile, int t0, int len, const void* safe) {
+        if (on) {
+            const char* x = src;
+            if (t0 + CQ <= len) {
+#pragma unroll
+                for (int i = 0; i < N; ++i, x += step) wm::cpa16(tile + dst + i * STEP * COLS * 2, x);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i, x += step) {
+                    const bool in = t0 + row + i * STEP < len;
+                    wm::cpa16(tile + dst + i * STEP * COLS * 2, in ? x : safe, !in);
+                }
+            }
+        }
+        src += step * N;
+    }
+};
 
-// a power of two that brings x (> 0) near 2^12, at most 2^40 (the fp32 sums that carry it stay
-// far from their limits); 1 for 0 and what is not finite
-__device__ __forceinline__ float to_middle(float x) {
+// a power of two that brings x (> 0) near 2^12, within 2^low and 2^high; 1 for 0 and what is
+// not finite
+__device__ __forceinline__ float to_middle(float x, int low, int high) {
     const int e = (__float_as_int(x) >> 23) & 255;
     if (e == 0 || e == 255) return 1.f;
-    return __int_as_float(min(max(254 - e + 12, 1), 127 + 40) << 23);
+    return __int_as_float((127 + min(max(127 - e + 12, low), high)) << 23);
 }
 
 // a decay of 0 drops what it multiplies, also what is not finite
 __device__ __forceinline__ float fade(float d, float x) { return d == 0.f ? 0.f : d * x; }
 
+template <typename T> struct Pair;
+template <> struct Pair<f16> { typedef __half2 type; };
+template <> struct Pair<bf16> { typedef __nv_bfloat162 type; };
 template <typename T>
-__device__ __forceinline__ bool odd2(uint32_t w) {
-    constexpr uint32_t E = std::is_same<T, bf16>::value ? 0x7f807f80u : 0x7c007c00u;
-    return __vcmpeq2(w & E, E) != 0;
+__device__ __forceinline__ typename Pair<T>::type pair(uint32_t x) {
+    return *reinterpret_cast<const typename Pair<T>::type*>(&x);
+}
+template <typename P2>
+__device__ __forceinline__ uint32_t bits(P2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+
+// the inverse of a power of two: its exponent mirrored
+__device__ __forceinline__ float inverse(float p) { return __int_as_float(0x7f000000 - __float_as_int(p)); }
+
+__device__ __forceinline__ void scale_rows(float (&x)[2][4], float a, float b) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        x[n][0] *= a;
+        x[n][1] *= a;
+        x[n][2] *= b;
+        x[n][3] *= b;
+    }
+}
+
+// sum_{j <= i} P_ij v_j of one value column, over the rows that i sees through a decay above 0
+template <typename T>
+__device__ __noinline__ float row_product(const Tables& tab, const uint8_t* p, const uint8_t* v, int i, int col) {
+    float sum = 0.f;
+    for (int j = 0; j <= i; ++j) {
+        if (fast_exp2(tab.a[i] + tab.b[i >> 4][j]) == 0.f) continue;
+        const T pj = *reinterpret_cast<const T*>(p + at<CQ>(i, j >> 3) + 2 * (j & 7));
+        const T vj = *reinterpret_cast<const T*>(v + at<CV>(j, col >> 3) + 2 * (col & 7));
+        sum = fmaf(to_f(pj), to_f(vj), sum);
+    }
+    return sum;
+}
+
+// the tables of one chunk from the two log decays each lane holds (rows 2 lane, 2 lane + 1)
+__device__ __forceinline__ void make_tables(Tables& t, float g0, float g1, float log2_scale) {
+    constexpr double LOG2E = 1.4426950408889634;
+    const int lane = threadIdx.x & 31;
+    // a decay below 2^-160 is 0 in fp32; the limit keeps -infinity out of the sums
+    const double d0 = g0 < -1.0e2f ? fmax((double)g0 * LOG2E, -160.0) : (double)g0 * LOG2E;
+    const double d1 = g1 < -1.0e2f ? fmax((double)g1 * LOG2E, -160.0) : (double)g1 * LOG2E;
+    double x1 = d0 + d1;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, x1, w);
+        if (lane >= w) x1 += y;
+    }
+    const double x0 = x1 - d1, last = __shfl_sync(0xffffffffu, x1, 31);
+    // (x1 - d1 loses nothing that matters: the sums stay below 2^14, their steps at 2^-39)
+    double from = 0.0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const double c = b == 0 ? 0.0 : __shfl_sync(0xffffffffu, x1, b == 0 ? 0 : 8 * b - 1);
+        if ((lane >> 3) == b) from = c;
+        if ((lane >> 3) <= b)
+            *reinterpret_cast<float2*>(&t.b[b][2 * lane]) = make_float2((float)(c - x0), (float)(c - x1));
+    }
+    *reinterpret_cast<float2*>(&t.a[2 * lane]) =
+        make_float2((float)(x0 - from) + log2_scale, (float)(x1 - from) + log2_scale);
+    *reinterpret_cast<float2*>(&t.e[2 * lane]) =
+        make_float2(fast_exp2((float)x0 + log2_scale), fast_exp2((float)x1 + log2_scale));
+    *reinterpret_cast<float2*>(&t.w[2 * lane]) =
+        make_float2(fast_exp2((float)(last - x0)), fast_exp2((float)(last - x1)));
+    const int grows = __any_sync(0xffffffffu, !(fmax(d0, d1) <= 0.0));
+    float down = fminf((float)d0, 0.f) + fminf((float)d1, 0.f);
+#pragma unroll
+    for (int w = 16; w; w >>= 1) down += __shfl_xor_sync(0xffffffffu, down, w);
+    if (lane == 0) {
+        t.dec = fast_exp2((float)last);
+        t.resets = !(down + fminf(log2_scale, 0.f) > -120.f);
+        t.grows = grows;
+    }
 }
 
 template <typename T, int DK>
@@ -90,9 +199,9 @@ __global__ void __launch_bounds__(NT, DK == 128 ? 2 : 3)
 linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict__ k, long long ldk,
                      const T* __restrict__ v, long long ldv, const float* __restrict__ g, long long ldg,
                      const int* __restrict__ cu, int total, const float* state_in, float* state_out,
-                     T* __restrict__ o, long long ldo, int Hk, int H, int dv, float scale, int* status) {
+                     T* __restrict__ o, long long ldo, int Hk, int H, int dv, float log2_scale, int* status) {
     constexpr bool F16 = std::is_same<T, f16>::value;
-    constexpr int NKT = DK / 8;  // 8-wide key tiles of the state
+    constexpr int NKT = DK / 8, KK = DK / 16;  // 8- and 16-wide key tiles
     griddep_sync();
     extern __shared__ __align__(128) uint8_t chunk_raw[];
     ChunkSmem<DK>& sm = *reinterpret_cast<ChunkSmem<DK>*>(chunk_raw);
@@ -103,21 +212,27 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
         if (tid == 0) set_status(status, HYMBA_ERR_DEVICE_RANGE);
         return;
     }
-    q += start * ldq + (long long)hk * DK;
-    k += start * ldk + (long long)hk * DK;
-    v += start * ldv + (long long)h * dv + c0;
-    o += start * ldo + (long long)h * dv + c0;
-    g += start * ldg + h;
     const int nchunk = (len + CQ - 1) / CQ;
+    Stager<T, DK> sq, sk;
+    Stager<T, CV> sv;
+    sq.init(q + start * ldq + (long long)hk * DK, ldq);
+    sk.init(k + start * ldk + (long long)hk * DK, ldk);
+    sv.init(v + start * ldv + (long long)h * dv + c0, ldv);
     auto load = [&](int c) {
-        stage<T, DK>(sm.q[c & 1], q, ldq, c * CQ, len);
-        stage<T, DK>(sm.k[c & 1], k, ldk, c * CQ, len);
-        stage<T, CV>(sm.v[c & 1], v, ldv, c * CQ, len);
+        sq.load(sm.q[c & 1], c * CQ, len, q);
+        sk.load(sm.k[c & 1], c * CQ, len, q);
+        sv.load(sm.v[c & 1], c * CQ, len, q);
     };
+    g += start * ldg + h;
     auto decay = [&](int t) { return t < len ? g[t * ldg] : 0.f; };
     if (nchunk > 0) load(0);
     wm::cpa_commit();
-    float g0 = decay(2 * lane), g1 = decay(2 * lane + 1);
+    float g0 = 0.f, g1 = 0.f;
+    if (warp == 0) {
+        if (nchunk > 0) make_tables(sm.tab[0], decay(2 * lane), decay(2 * lane + 1), log2_scale);
+        g0 = decay(CQ + 2 * lane);
+        g1 = decay(CQ + 2 * lane + 1);
+    }
     // S[value c0 + 16 warp + lg (+8)][key 8 n + 2 lq (+1)]
     float st[NKT][4];
     const long long sbase = (((long long)s * H + h) * dv + c0 + 16 * warp + lg) * DK + 2 * lq;
@@ -130,66 +245,82 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
         }
         st[n][0] = a.x; st[n][1] = a.y; st[n][2] = b.x; st[n][3] = b.y;
     }
+    // per-lane offsets of the ldmatrix pieces: rows lane % 16 at column half lane / 16 (A operands,
+    // transposed B operands), and rows of two 8-row tiles at column half (lane / 8) % 2 (B operands)
+    uint32_t xa[KK], xb[KK], xp[4];
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+        xa[kk] = at<DK>(lane & 15, 2 * kk + (lane >> 4));
+        xb[kk] = at<DK>((lane & 7) + 8 * (lane >> 4), 2 * kk + ((lane >> 3) & 1));
+    }
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) xp[kk] = at<CQ>(lane & 15, 2 * kk + (lane >> 4));
+    const uint32_t xv = at<CV>(lane & 15, 2 * warp + (lane >> 4));
+    T* orow = o + (start + (long long)lg) * ldo + (long long)h * dv + c0 + 16 * warp + 2 * lq;
 
     for (int c = 0; c < nchunk; ++c) {
         const int buf = c & 1, t0 = c * CQ;
         wm::cpa_wait0();
-        __syncthreads();  // chunk c is staged; chunk c - 1's stage and P are free
+        __syncthreads();  // chunk c and its tables are there; chunk c - 1's stage, tables and P are free
         if (c + 1 < nchunk) load(c + 1);
         wm::cpa_commit();
-        // ---- decays: inclusive sums of the chunk's rows, every warp for itself ----
-        {
-            // a decay below 2^-160 is 0 in fp32; the limit keeps -infinity out of the sums
-            const double d0 = fmax((double)g0 * LOG2E, -160.0), d1 = fmax((double)g1 * LOG2E, -160.0);
-            double x = (g0 != g0 ? (double)g0 : d0) + (g1 != g1 ? (double)g1 : d1);
-            const double mine1 = g1 != g1 ? (double)g1 : d1;
-#pragma unroll
-            for (int w = 1; w < 32; w <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, x, w);
-                if (lane >= w) x += y;
-            }
-            const double x0 = x - mine1;
-            const float a = (float)x0, b = (float)x;
-            *reinterpret_cast<float4*>(&sm.cs[warp][2 * lane]) = make_float4(a, (float)(x0 - a), b, (float)(x - b));
-            if (c + 1 < nchunk) {
-                g0 = decay(t0 + CQ + 2 * lane);
-                g1 = decay(t0 + CQ + 2 * lane + 1);
-            }
+        const uint8_t *qs = sm.q[buf], *ks = sm.k[buf], *vs = sm.v[buf];
+        const Tables& tab = sm.tab[buf];
+        const bool resets = tab.resets;
+        if (warp == 0 && c + 1 < nchunk) {
+            make_tables(sm.tab[buf ^ 1], g0, g1, log2_scale);
+            g0 = decay(t0 + 2 * CQ + 2 * lane);
+            g1 = decay(t0 + 2 * CQ + 2 * lane + 1);
         }
-        __syncwarp();
-        const float2* cs = sm.cs[warp];
         // ---- P: rows 16 warp + lg (+8) ----
         {
-            const int r0 = 16 * warp;
-            const float2 ci0 = cs[r0 + lg], ci1 = cs[r0 + lg + 8];
+            const float a0 = tab.a[16 * warp + lg], a1 = tab.a[16 * warp + lg + 8];
             float pr[4][2][4];
             float mx0 = 0.f, mx1 = 0.f;
-            uint32_t qf[DK / 16][4];
 #pragma unroll
-            for (int kk = 0; kk < DK / 16; ++kk)
-                wm::ldsm_x4(qf[kk], sm.q[buf] + at<DK>(r0 + (lane & 15), 2 * kk + (lane >> 4)));
-#pragma unroll
-            for (int jt = 0; jt < 4; ++jt) {
+            for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) pr[jt][0][e] = pr[jt][1][e] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                uint32_t qf[4];
+                wm::ldsm_x4(qf, qs + warp * 16 * DK * 2 + xa[kk]);
+#pragma unroll
+                for (int jt = 0; jt < 4; ++jt)
+                    if (jt <= warp) {
+                        uint32_t kf[4];
+                        wm::ldsm_x4(kf, ks + jt * 16 * DK * 2 + xb[kk]);
+                        wm::mma16<T>(pr[jt][0], qf, kf[0], kf[1]);
+                        wm::mma16<T>(pr[jt][1], qf, kf[2], kf[3]);
+                    }
+            }
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt) {
                 if (jt <= warp) {
 #pragma unroll
-                    for (int kk = 0; kk < DK / 16; ++kk) {
-                        uint32_t kf[4];
-                        wm::ldsm_x4(kf, sm.k[buf] + at<DK>(16 * jt + (lane & 7) + 8 * (lane >> 4), 2 * kk + ((lane >> 3) & 1)));
-                        wm::mma16<T>(pr[jt][0], qf[kk], kf[0], kf[1]);
-                        wm::mma16<T>(pr[jt][1], qf[kk], kf[2], kf[3]);
-                    }
-#pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        const int j = 16 * jt + 8 * n + 2 * lq;
-                        const float4 cj = *reinterpret_cast<const float4*>(&cs[j]);
-                        const int i = r0 + lg;
+                        const float2 bj = *reinterpret_cast<const float2*>(&tab.b[warp][16 * jt + 8 * n + 2 * lq]);
                         float* p = pr[jt][n];
-                        p[0] = j <= i ? fade(fast_exp2((ci0.x - cj.x) + (ci0.y - cj.y)), p[0] * scale) : 0.f;
-                        p[1] = j + 1 <= i ? fade(fast_exp2((ci0.x - cj.z) + (ci0.y - cj.w)), p[1] * scale) : 0.f;
-                        p[2] = j <= i + 8 ? fade(fast_exp2((ci1.x - cj.x) + (ci1.y - cj.y)), p[2] * scale) : 0.f;
-                        p[3] = j + 1 <= i + 8 ? fade(fast_exp2((ci1.x - cj.z) + (ci1.y - cj.w)), p[3] * scale) : 0.f;
+                        const float w0 = fast_exp2(a0 + bj.x), w1 = fast_exp2(a0 + bj.y);
+                        const float w2 = fast_exp2(a1 + bj.x), w3 = fast_exp2(a1 + bj.y);
+                        if (!resets) {
+                            p[0] *= w0;
+                            p[1] *= w1;
+                            p[2] *= w2;
+                            p[3] *= w3;
+                        } else {
+                            p[0] = fade(w0, p[0]);
+                            p[1] = fade(w1, p[1]);
+                            p[2] = fade(w2, p[2]);
+                            p[3] = fade(w3, p[3]);
+                        }
+                        if (jt == warp) {
+                            const int j = 8 * n + 2 * lq;
+                            p[0] = j <= lg ? p[0] : 0.f;
+                            p[1] = j + 1 <= lg ? p[1] : 0.f;
+                            p[2] = j <= lg + 8 ? p[2] : 0.f;
+                            p[3] = j + 1 <= lg + 8 ? p[3] : 0.f;
+                        }
                         if (F16) {
                             mx0 = fmaxf(mx0, fmaxf(fabsf(p[0]), fabsf(p[1])));
                             mx1 = fmaxf(mx1, fmaxf(fabsf(p[2]), fabsf(p[3])));
@@ -204,25 +335,27 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
                     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, w));
                     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, w));
                 }
-                f0 = to_middle(mx0);
-                f1 = to_middle(mx1);
+                f0 = to_middle(mx0, -40, 40);
+                f1 = to_middle(mx1, -40, 40);
                 if (lq == 0) {
-                    sm.ps[r0 + lg] = f0;
-                    sm.ps[r0 + lg + 8] = f1;
+                    sm.ps[16 * warp + lg] = f0;
+                    sm.ps[16 * warp + lg + 8] = f1;
                 }
             }
+            uint8_t* pw = sm.p + (16 * warp + lg) * CQ * 2 + 4 * lq;
 #pragma unroll
             for (int jt = 0; jt < 4; ++jt)
                 if (jt <= warp)
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        uint8_t* a = sm.p + at<CQ>(r0 + lg, 2 * jt + n) + 4 * lq;
-                        uint8_t* b = sm.p + at<CQ>(r0 + lg + 8, 2 * jt + n) + 4 * lq;
-                        *reinterpret_cast<uint32_t*>(a) = pack2<T>(pr[jt][n][0] * f0, pr[jt][n][1] * f0);
-                        *reinterpret_cast<uint32_t*>(b) = pack2<T>(pr[jt][n][2] * f1, pr[jt][n][3] * f1);
+                        uint8_t* x = pw + ((2 * jt + n) ^ lg) * 16;
+                        const float* p = pr[jt][n];
+                        *reinterpret_cast<uint32_t*>(x) = F16 ? pack2<T>(p[0] * f0, p[1] * f0) : pack2<T>(p[0], p[1]);
+                        *reinterpret_cast<uint32_t*>(x + 8 * CQ * 2) =
+                            F16 ? pack2<T>(p[2] * f1, p[3] * f1) : pack2<T>(p[2], p[3]);
                     }
         }
-        // ---- exp(cs_i) scale S q_i for this warp's value columns ----
+        // ---- 2^cs_i scale S q_i for this warp's value columns ----
         float out[4][2][4];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
@@ -238,81 +371,77 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
                     for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(st[n][e]));
 #pragma unroll
                 for (int w = 1; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-                fs = to_middle(mx);
+                fs = to_middle(mx, -100, 100);
             }
+            auto part = [&](float x, float y) { return F16 ? pack2<T>(x * fs, y * fs) : pack2<T>(x, y); };
 #pragma unroll
-            for (int kk = 0; kk < DK / 16; ++kk) {
-                const uint32_t b0 = pack2<T>(st[2 * kk][0] * fs, st[2 * kk][1] * fs);
-                const uint32_t b1 = pack2<T>(st[2 * kk + 1][0] * fs, st[2 * kk + 1][1] * fs);
-                const uint32_t b2 = pack2<T>(st[2 * kk][2] * fs, st[2 * kk][3] * fs);
-                const uint32_t b3 = pack2<T>(st[2 * kk + 1][2] * fs, st[2 * kk + 1][3] * fs);
+            for (int kk = 0; kk < KK; ++kk) {
+                const uint32_t b0 = part(st[2 * kk][0], st[2 * kk][1]), b1 = part(st[2 * kk + 1][0], st[2 * kk + 1][1]);
+                const uint32_t b2 = part(st[2 * kk][2], st[2 * kk][3]), b3 = part(st[2 * kk + 1][2], st[2 * kk + 1][3]);
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
                     uint32_t qf[4];
-                    wm::ldsm_x4(qf, sm.q[buf] + at<DK>(16 * mt + (lane & 15), 2 * kk + (lane >> 4)));
+                    wm::ldsm_x4(qf, qs + mt * 16 * DK * 2 + xa[kk]);
                     wm::mma16<T>(out[mt][0], qf, b0, b1);
                     wm::mma16<T>(out[mt][1], qf, b2, b3);
                 }
             }
-            const float back = scale / fs;
+            const float back = F16 ? 1.f / fs : 1.f;
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                const float2 a = cs[16 * mt + lg], b = cs[16 * mt + lg + 8];
-                const float ea = fast_exp2(a.x + a.y), eb = fast_exp2(b.x + b.y);
+                const float ea = tab.e[16 * mt + lg] * back, eb = tab.e[16 * mt + lg + 8] * back;
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    out[mt][n][0] = fade(ea, out[mt][n][0] * back);
-                    out[mt][n][1] = fade(ea, out[mt][n][1] * back);
-                    out[mt][n][2] = fade(eb, out[mt][n][2] * back);
-                    out[mt][n][3] = fade(eb, out[mt][n][3] * back);
+                    if (!resets) {
+                        out[mt][n][0] *= ea;
+                        out[mt][n][1] *= ea;
+                        out[mt][n][2] *= eb;
+                        out[mt][n][3] *= eb;
+                    } else {
+                        out[mt][n][0] = fade(ea, out[mt][n][0]);
+                        out[mt][n][1] = fade(ea, out[mt][n][1]);
+                        out[mt][n][2] = fade(eb, out[mt][n][2]);
+                        out[mt][n][3] = fade(eb, out[mt][n][3]);
+                    }
                 }
             }
         }
         // ---- V fragments: B operand (rows j x 16 value columns), and V^T as the A operand ----
         uint32_t vf[4][4];
-        bool odd = false;
+        bool odd;
+        {
+            auto zero = pair<T>(0u), any = zero;  // 0 x (not finite) is NaN
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            wm::ldsm_x4_t(vf[kk], sm.v[buf] + at<CV>(16 * kk + (lane & 7) + 8 * ((lane >> 3) & 1), 2 * warp + (lane >> 4)));
+            for (int kk = 0; kk < 4; ++kk) {
+                wm::ldsm_x4_t(vf[kk], vs + kk * 16 * CV * 2 + xv);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) odd |= odd2<T>(vf[kk][e]);
+                for (int e = 0; e < 4; ++e) any = __hfma2(pair<T>(vf[kk][e]), zero, any);
+            }
+            odd = __any_sync(0xffffffffu, (bits(any) & 0x7fff7fffu) != 0);
         }
-        odd = __any_sync(0xffffffffu, odd);
         __syncthreads();  // P is there
         // ---- + P V ----
         if (!odd) {
+            if (F16) {
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                float fa = 1.f, fb = 1.f;
-                if (F16) {
-                    fa = sm.ps[16 * mt + lg];
-                    fb = sm.ps[16 * mt + lg + 8];
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        out[mt][n][0] *= fa;
-                        out[mt][n][1] *= fa;
-                        out[mt][n][2] *= fb;
-                        out[mt][n][3] *= fb;
-                    }
+                for (int mt = 0; mt < 4; ++mt) {
+                    const float fa = sm.ps[16 * mt + lg], fb = sm.ps[16 * mt + lg + 8];
+                    scale_rows(out[mt], fa, fb);
                 }
+            }
 #pragma unroll
-                for (int kk = 0; kk <= mt; ++kk) {
+            for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                for (int mt = kk; mt < 4; ++mt) {
                     uint32_t pf[4];
-                    wm::ldsm_x4(pf, sm.p + at<CQ>(16 * mt + (lane & 15), 2 * kk + (lane >> 4)));
+                    wm::ldsm_x4(pf, sm.p + mt * 16 * CQ * 2 + xp[kk]);
                     wm::mma16<T>(out[mt][0], pf, vf[kk][0], vf[kk][1]);
                     wm::mma16<T>(out[mt][1], pf, vf[kk][2], vf[kk][3]);
                 }
-                if (F16) {
-                    fa = 1.f / fa;
-                    fb = 1.f / fb;
+            if (F16) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        out[mt][n][0] *= fa;
-                        out[mt][n][1] *= fa;
-                        out[mt][n][2] *= fb;
-                        out[mt][n][3] *= fb;
-                    }
-                }
+                for (int mt = 0; mt < 4; ++mt)
+                    scale_rows(out[mt], inverse(sm.ps[16 * mt + lg]), inverse(sm.ps[16 * mt + lg + 8]));
             }
         } else {
 #pragma unroll
@@ -320,92 +449,84 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int n = e >> 2, i = 16 * mt + lg + 8 * ((e >> 1) & 1), col = 16 * warp + 8 * n + 2 * lq + (e & 1);
-                    const float2 ci = cs[i];
-                    float sum = 0.f;
-#pragma unroll 1
-                    for (int j = 0; j <= i; ++j) {
-                        const float2 cj = cs[j];
-                        if (fast_exp2((ci.x - cj.x) + (ci.y - cj.y)) == 0.f) continue;
-                        const T pj = *reinterpret_cast<const T*>(sm.p + at<CQ>(i, j >> 3) + 2 * (j & 7));
-                        const T vj = *reinterpret_cast<const T*>(sm.v[buf] + at<CV>(j, col >> 3) + 2 * (col & 7));
-                        sum = fmaf(to_f(pj), to_f(vj), sum);
-                    }
-                    out[mt][n][e & 3] += F16 ? sum / sm.ps[i] : sum;
+                    const float x = row_product<T>(tab, sm.p, vs, i, col);
+                    out[mt][n][e & 3] += F16 ? x / sm.ps[i] : x;
                 }
         }
         // ---- o ----
+        {
+            T* x = orow;
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int i = t0 + 16 * mt + lg + 8 * half;
-                if (i < len)
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-                        *reinterpret_cast<uint32_t*>(o + i * ldo + 16 * warp + 8 * n + 2 * lq) =
-                            pack2<T>(out[mt][n][2 * half], out[mt][n][2 * half + 1]);
+            for (int r = 0; r < 8; ++r, x += 8 * ldo) {
+                if (t0 + 8 * r + lg < len) {
+                    const float* y = out[r >> 1][0] + 2 * (r & 1);
+                    *reinterpret_cast<uint32_t*>(x) = pack2<T>(y[0], y[1]);
+                    *reinterpret_cast<uint32_t*>(x + 8) = pack2<T>(y[4], y[5]);
+                }
             }
+            orow = x;
+        }
         // ---- state ----
         {
-            const float2 cl = cs[CQ - 1];
-            const float dec = fast_exp2(cl.x + cl.y);
-            float w[4][4];  // exp(cs_64 - cs_j) of rows 16 kk + 2 lq, + 1, + 8, + 9
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float4 cj = *reinterpret_cast<const float4*>(&cs[16 * kk + 2 * lq + 8 * x]);
-                    w[kk][2 * x] = fast_exp2((cl.x - cj.x) + (cl.y - cj.y));
-                    w[kk][2 * x + 1] = fast_exp2((cl.x - cj.z) + (cl.y - cj.w));
-                }
-            auto scaled = [&](int kk, int e, float* x0, float* x1) {
-                // fragment e: rows + 8 for odd e (the second row half of the ldmatrix pair)
-                const T* x = reinterpret_cast<const T*>(&vf[kk][e]);
-                *x0 = fade(w[kk][2 * (e & 1)], to_f(x[0]));
-                *x1 = fade(w[kk][2 * (e & 1) + 1], to_f(x[1]));
-            };
             float fv = 1.f;
             if (F16) {
-                float mx = 0.f;
+                auto mx = __habs2(pair<T>(vf[0][0]));
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
+                for (int x = 1; x < 16; ++x) mx = __hmax2(mx, __habs2(pair<T>(vf[x >> 2][x & 3])));
+                float m = fmaxf(__low2float(mx), __high2float(mx));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x0, x1;
-                        scaled(kk, e, &x0, &x1);
-                        mx = fmaxf(mx, fmaxf(fabsf(x0), fabsf(x1)));
-                    }
+                for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                // (never down, where it would cost small values their last bits, unless a weight is above 1)
+                fv = to_middle(m, tab.grows ? -15 : 0, 15);
+                const auto f2 = pair<T>(pack2<T>(fv, fv));
 #pragma unroll
-                for (int x = 1; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-                fv = to_middle(mx);
+                for (int x = 0; x < 16; ++x) vf[x >> 2][x & 3] = bits(__hmul2(pair<T>(vf[x >> 2][x & 3]), f2));
+            }
+            const float dec = tab.dec * fv;
+            if (!resets) {
+#pragma unroll
+                for (int n = 0; n < NKT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) st[n][e] *= dec;
+            } else {
+#pragma unroll
+                for (int n = 0; n < NKT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) st[n][e] = fade(dec, st[n][e]);
             }
 #pragma unroll
-            for (int n = 0; n < NKT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) st[n][e] = fade(dec, st[n][e]) * fv;
-#pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
+                uint32_t kf[KK][4];
+#pragma unroll
+                for (int n = 0; n < KK; ++n) wm::ldsm_x4_t(kf[n], ks + kk * 16 * DK * 2 + xa[n]);
                 uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // A operand order: (values 0-7, rows 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
-                    const int from = ((e & 1) << 1) | (e >> 1);
-                    float x0, x1;
-                    scaled(kk, from, &x0, &x1);
-                    wm::split2<T>(x0 * fv, x1 * fv, &hi[e], &lo[e]);
+                for (int x = 0; x < 2; ++x) {
+                    const float2 w = *reinterpret_cast<const float2*>(&tab.w[16 * kk + 8 * x + 2 * lq]);
+                    uint32_t keep = 0xffffffffu;
+                    if (resets) keep = (w.x == 0.f ? 0u : 0x0000ffffu) | (w.y == 0.f ? 0u : 0xffff0000u);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        // V fragment (values 8 y .., rows 8 x ..) is operand part 2 x + y
+                        const uint32_t vv = resets ? vf[kk][2 * y + x] & keep : vf[kk][2 * y + x];
+                        const T* e = reinterpret_cast<const T*>(&vv);
+                        const float2 z = __fmul2_rn(make_float2(to_f(e[0]), to_f(e[1])), w);
+                        wm::split2<T>(z.x, z.y, &hi[2 * x + y], &lo[2 * x + y]);
+                    }
                 }
 #pragma unroll
-                for (int n2 = 0; n2 < DK / 16; ++n2) {
-                    uint32_t kf[4];
-                    wm::ldsm_x4_t(kf, sm.k[buf] + at<DK>(16 * kk + (lane & 7) + 8 * ((lane >> 3) & 1), 2 * n2 + (lane >> 4)));
-                    wm::mma16<T>(st[2 * n2], hi, kf[0], kf[1]);
-                    wm::mma16<T>(st[2 * n2 + 1], hi, kf[2], kf[3]);
-                    wm::mma16<T>(st[2 * n2], lo, kf[0], kf[1]);
-                    wm::mma16<T>(st[2 * n2 + 1], lo, kf[2], kf[3]);
+                for (int n = 0; n < KK; ++n) {
+                    wm::mma16<T>(st[2 * n], hi, kf[n][0], kf[n][1]);
+                    wm::mma16<T>(st[2 * n + 1], hi, kf[n][2], kf[n][3]);
+                }
+#pragma unroll
+                for (int n = 0; n < KK; ++n) {
+                    wm::mma16<T>(st[2 * n], lo, kf[n][0], kf[n][1]);
+                    wm::mma16<T>(st[2 * n + 1], lo, kf[n][2], kf[n][3]);
                 }
             }
             if (F16) {
-                const float back = 1.f / fv;
+                const float back = inverse(fv);
 #pragma unroll
                 for (int n = 0; n < NKT; ++n)
 #pragma unroll
@@ -436,7 +557,7 @@ int launch_dk(const Ctx& ctx, const LinAttn& a) {
         HYMBA_LAUNCH(ctx, "linattn_chunk", kern, dim3(a.dv / CV, a.H, n), NT, smem, static_cast<const T*>(a.q), a.ldq,
                      static_cast<const T*>(a.k), a.ldk, static_cast<const T*>(a.v), a.ldv, a.g, a.ldg, a.cu + s0,
                      a.total, a.state_in ? a.state_in + st0 : nullptr, a.state_out ? a.state_out + st0 : nullptr,
-                     static_cast<T*>(a.o), a.ldo, a.Hk, a.H, a.dv, a.scale, ctx.status);
+                     static_cast<T*>(a.o), a.ldo, a.Hk, a.H, a.dv, log2f(a.scale), ctx.status);
     }
     return HYMBA_OK;
 }
