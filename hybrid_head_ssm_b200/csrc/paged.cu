@@ -29,9 +29,11 @@ struct AppendArgs {
     int kshift, vshift;  // log2 of the 16-byte pieces of one head's row
 };
 
-// One warp per row: its sequence by binary search, its slot from the page table, then
-// 16-byte pieces from the row into the heads' slots. Bound by HBM: every byte is read
-// once and written once.
+// RW rows per warp: lane i looks up row i (its sequence by binary search, its slot from the
+// page table), then the warp moves 16-byte pieces from the rows into the heads' slots, eight
+// per lane in flight. Bound by HBM for prompts (every byte is read once and written once), by
+// the chain of lookups for single tokens.
+template <int RW>
 __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int* status) {
     griddep_sync();
     if (a.cu && blockIdx.x == 0)
@@ -39,43 +41,69 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int*
             int st, n;
             if (!ragged::sequence(a.cu, s, a.rows, &st, &n)) set_status(status, HYMBA_ERR_DEVICE_RANGE);
         }
-    const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const long long r0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * RW;
     const int lane = threadIdx.x & 31;
-    if (r >= a.rows) return;
-    int b = (int)r, back = 1;  // the row is position len - back of sequence b
-    if (a.cu) {
-        int lo = 0, hi = a.batch;  // the last sequence that starts at or before r
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.cu[mid] <= r) lo = mid;
-            else hi = mid;
+    if (r0 >= a.rows) return;
+    long long slot = -1;  // of KV head 0; head g is g * page further
+    const long long r = r0 + min(lane, RW - 1);
+    if (r < a.rows) {
+        int b = (int)r, back = 1;  // the row is position len - back of sequence b
+        bool mine = true;
+        if (a.cu) {
+            int lo = 0, hi = a.batch;  // the last sequence that starts at or before r
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (a.cu[mid] <= r) lo = mid;
+                else hi = mid;
+            }
+            b = lo;
+            int st, n;
+            mine = ragged::sequence(a.cu, b, a.rows, &st, &n) && r >= st && r < st + n;
+            back = (int)(st + n - r);
         }
-        b = lo;
-        int st, n;
-        if (!ragged::sequence(a.cu, b, a.rows, &st, &n) || r < st || r >= st + n) return;
-        back = (int)(st + n - r);
+        if (mine) {
+            const int len = a.len[b];
+            const long long pos = (long long)len - back;
+            int at = -1;
+            if (pos >= 0 && len <= (long long)a.max_pages * a.page)
+                at = a.table[(long long)b * a.max_pages + (int)pos / a.page];
+            if (at >= 0 && at < a.n_pages) slot = (long long)at * a.G * a.page + (int)pos % a.page;
+            else if (lane < RW) set_status(status, HYMBA_ERR_DEVICE_RANGE);
+        }
     }
-    const int len = a.len[b];
-    const long long pos = (long long)len - back;
-    int at = -1;
-    if (pos >= 0 && len <= (long long)a.max_pages * a.page)
-        at = a.table[(long long)b * a.max_pages + (int)pos / a.page];
-    if (at < 0 || at >= a.n_pages) {
-        if (lane == 0) set_status(status, HYMBA_ERR_DEVICE_RANGE);
-        return;
-    }
-    const long long slot = (long long)at * a.G * a.page + (int)pos % a.page;  // + g * page: the head's row
-    const uint8_t* kr = a.k + r * a.ldk;
-    const uint8_t* vr = a.v + r * a.ldv;
-    for (int c = lane; c < a.G << a.kshift; c += 32) {
-        const int g = c >> a.kshift, e = c & ((1 << a.kshift) - 1);
-        *reinterpret_cast<uint4*>(a.k_pages + (((slot + (long long)g * a.page) << a.kshift) + e) * 16) =
-            *reinterpret_cast<const uint4*>(kr + c * 16);
-    }
-    for (int c = lane; c < a.G << a.vshift; c += 32) {
-        const int g = c >> a.vshift, e = c & ((1 << a.vshift) - 1);
-        *reinterpret_cast<uint4*>(a.v_pages + (((slot + (long long)g * a.page) << a.vshift) + e) * 16) =
-            *reinterpret_cast<const uint4*>(vr + c * 16);
+    const int nk = a.G << a.kshift, n = nk + (a.G << a.vshift);  // pieces of a row: K's, then V's
+    constexpr int U = 4, RB = RW > 1 ? 2 : 1;  // pieces per lane, rows at a time
+#pragma unroll 1
+    for (int i = 0; i < RW; i += RB) {
+        if (r0 + i >= a.rows) break;
+        long long sl[RB];
+#pragma unroll
+        for (int y = 0; y < RB; ++y) sl[y] = __shfl_sync(0xffffffffu, slot, i + y);
+#pragma unroll 1
+        for (int c0 = 0; c0 < n; c0 += 32 * U) {
+            uint4 w[RB][U];
+#pragma unroll
+            for (int y = 0; y < RB; ++y)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int c = c0 + 32 * u + lane;
+                    if (c < n && sl[y] >= 0)
+                        w[y][u] = __ldg(reinterpret_cast<const uint4*>(c < nk ? a.k + (r0 + i + y) * a.ldk + c * 16
+                                                                             : a.v + (r0 + i + y) * a.ldv + (c - nk) * 16));
+                }
+#pragma unroll
+            for (int y = 0; y < RB; ++y)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int c = c0 + 32 * u + lane;
+                    if (c >= n || sl[y] < 0) continue;
+                    const bool is_k = c < nk;
+                    const int e = is_k ? c : c - nk, sh = is_k ? a.kshift : a.vshift;
+                    const int g = e >> sh, f = e & ((1 << sh) - 1);
+                    *reinterpret_cast<uint4*>((is_k ? a.k_pages : a.v_pages) +
+                                              (((sl[y] + (long long)g * a.page) << sh) + f) * 16) = w[y][u];
+                }
+        }
     }
 }
 
@@ -120,6 +148,8 @@ __device__ __forceinline__ long long slot_of(const DecodeArgs<T>& a, int b, int 
 // of its query heads, sequence). Chunks of 128 keys: a thread forms one key's scores, two
 // heads' softmax per warp, then a thread owns a column of V.
 constexpr int SC = 128, SR = 8;
+constexpr int MAX_CL = 8;        // splits that join as one cluster
+constexpr int MAX_SPLITS = 64;   // splits of one sequence
 
 template <typename T, int DH, int DV>
 __global__ void __launch_bounds__(128) decode_paged_simt_kernel(const DecodeArgs<T> a, int* status) {
@@ -251,14 +281,20 @@ __global__ void __launch_bounds__(128) decode_paged_simt_kernel(const DecodeArgs
 // past the split's last key are zero-filled by the copy and masked. Bound by HBM: K and V
 // of every visible key once.
 constexpr int TK = 16;                 // keys per tile
-constexpr int RING = 24 * 1024;        // bytes of one warp's ring
+// Three blocks per SM with 72 KB (64 KB) of rings each where a tile has at most 192 (128)
+// dims, two with 96 KB at 256. 64 sequences of the 1.5B heads, window 1024: 33.0 us against 36.0
+// with two blocks of four stages; 16 long contexts 100.9 against 115.4.
 template <int DH, int DV>
 struct Ring {
-    static constexpr int KB = TK * DH * 2, VB = TK * DV * 2, BYTES = KB + VB, N = RING / BYTES;
+    static constexpr int KB = TK * DH * 2, VB = TK * DV * 2, BYTES = KB + VB;
+    static constexpr int N = DH + DV == 128 ? 4 : 3, SIZE = N * BYTES;  // stages and bytes of one warp's ring
 };
+constexpr int blocks_per_sm(int dims, int ng) { return dims <= 192 && ng == 1 ? 3 : 2; }
 
-template <typename T, int DH, int DV, int NG>
-__global__ void __launch_bounds__(128, 2) decode_paged_mma_kernel(const DecodeArgs<T> a, int* status) {
+// CL: the splits of one (KV head, sequence) form a thread-block cluster and join over distributed
+// shared memory; otherwise they leave partial results for the join kernel.
+template <typename T, int DH, int DV, int NG, bool CL>
+__global__ void __launch_bounds__(128, blocks_per_sm(DH + DV, NG)) decode_paged_mma_kernel(const DecodeArgs<T> a, int* status) {
     using R_ = Ring<DH, DV>;
     griddep_sync();
     extern __shared__ __align__(128) uint8_t decode_raw[];
@@ -272,9 +308,9 @@ __global__ void __launch_bounds__(128, 2) decode_paged_mma_kernel(const DecodeAr
     const bool fine = view_of(a, b, &w);
     if (!fine && split == 0 && blockIdx.y == 0 && tid == 0) set_status(status, HYMBA_ERR_DEVICE_RANGE);
     const int k0 = split * a.split_keys, k1 = min(w.n, k0 + a.split_keys);
-    if (k0 >= k1 && split > 0) return;
+    if (!CL && k0 >= k1 && split > 0) return;
     const int ntile = k1 > k0 ? (k1 - k0 + TK - 1) / TK : 0;
-    uint8_t* ring = decode_raw + warp * RING;
+    uint8_t* ring = decode_raw + warp * R_::SIZE;
 
     // q as the "col" operand: heads x dims
     uint32_t qf[NG][DH / 16][2];
@@ -439,7 +475,7 @@ __global__ void __launch_bounds__(128, 2) decode_paged_mma_kernel(const DecodeAr
     if (bad && tid == 0) set_status(status, HYMBA_ERR_DEVICE_RANGE);
     constexpr int LD = DV + 4;
     float* acc = reinterpret_cast<float*>(decode_raw);  // [4][8 NG][LD]
-    static_assert(4 * 8 * NG * LD * 4 <= 4 * RING, "the joined sums reuse the rings");
+    static_assert(4 * 8 * NG * LD * 4 <= 4 * R_::SIZE, "the joined sums reuse the rings");
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
         float f[2];
@@ -461,96 +497,187 @@ __global__ void __launch_bounds__(128, 2) decode_paged_mma_kernel(const DecodeAr
         }
     }
     __syncthreads();
-    for (int x = tid; x < nh * DV; x += 128) {
-        const int h = x / DV, col = x % DV;
-        float to = fmaxf(fmaxf(ms[0][h], ms[1][h]), fmaxf(ms[2][h], ms[3][h]));
-        float sum = 0.f, lt = 0.f;
+    auto joined = [&](int h, float* to, float* lt) {
+        *to = fmaxf(fmaxf(ms[0][h], ms[1][h]), fmaxf(ms[2][h], ms[3][h]));
+        *lt = 0.f;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            sum += acc[(v * 8 * NG + h) * LD + col];
-            lt += ms[v][h] == -INFINITY ? ls[v][h] : ls[v][h] * fast_exp2(ms[v][h] - to);
+        for (int v = 0; v < 4; ++v) *lt += ms[v][h] == -INFINITY ? ls[v][h] : ls[v][h] * fast_exp2(ms[v][h] - *to);
+    };
+    if constexpr (CL) {
+        // the block's sums, max and sum of p per head, read by every block of the cluster, each
+        // of which writes its share of the outputs
+        for (int x = tid; x < nh * DV; x += 128) {
+            float* p = acc + x / DV * LD + x % DV;
+            *p = p[0] + p[8 * NG * LD] + p[16 * NG * LD] + p[24 * NG * LD];
         }
-        if (a.n_split == 1) {
-            a.o[b * a.ldo + (long long)(h0 + h) * DV + col] = from_f<T>(bad || lt == 0.f ? 0.f : sum / lt);
-        } else {
-            float* p = a.part + (((long long)b * a.H + h0 + h) * a.n_split + split) * (DV + 4);
-            p[col] = sum;
-            if (col == 0) {
-                p[DV] = to;
-                p[DV + 1] = bad ? -1.f : lt;
+        if (tid < nh) {
+            float to, lt;
+            joined(tid, &to, &lt);
+            acc[tid * LD + DV] = to;
+            acc[tid * LD + DV + 1] = bad ? -1.f : lt;
+        }
+        cluster_arrive();
+        cluster_wait();
+        for (int x = split * 128 + tid; x < nh * DV; x += 128 * a.n_split) {
+            const int h = x / DV, col = x % DV;
+            float mm[MAX_CL], to = -INFINITY, lt = 0.f, sum = 0.f;
+            bool any_bad = false;
+#pragma unroll
+            for (int r = 0; r < MAX_CL; ++r) {
+                mm[r] = r < a.n_split ? ld_cluster_f32(acc + h * LD + DV, r) : -INFINITY;
+                to = fmaxf(to, mm[r]);
+            }
+            const float mu = to == -INFINITY ? 0.f : to;
+#pragma unroll
+            for (int r = 0; r < MAX_CL; ++r)
+                if (r < a.n_split) {
+                    const float lr = ld_cluster_f32(acc + h * LD + DV + 1, r), f = fast_exp2(mm[r] - mu);
+                    any_bad |= lr < 0.f;
+                    lt = fmaf(lr, f, lt);
+                    sum = fmaf(ld_cluster_f32(acc + h * LD + col, r), f, sum);
+                }
+            a.o[b * a.ldo + (long long)(h0 + h) * DV + col] = from_f<T>(any_bad || lt == 0.f ? 0.f : sum / lt);
+        }
+        cluster_arrive();
+        cluster_wait();  // no block leaves while another reads its shared memory
+    } else {
+        for (int x = tid; x < nh * DV; x += 128) {
+            const int h = x / DV, col = x % DV;
+            float sum = 0.f, to, lt;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) sum += acc[(v * 8 * NG + h) * LD + col];
+            joined(h, &to, &lt);
+            if (a.n_split == 1) {
+                a.o[b * a.ldo + (long long)(h0 + h) * DV + col] = from_f<T>(bad || lt == 0.f ? 0.f : sum / lt);
+            } else {
+                float* p = a.part + (((long long)b * a.H + h0 + h) * a.n_split + split) * (DV + 4);
+                p[col] = sum;
+                if (col == 0) {
+                    p[DV] = to;
+                    p[DV + 1] = bad ? -1.f : lt;
+                }
             }
         }
     }
 }
 
-// Join the key splits of one (query head, sequence): weights 2^(m_s - max m).
+// Join the key splits of one (query head, sequence): weights 2^(m_s - max m), then the
+// splits' sums, 256 / DV of them at a time per column.
 template <typename T, int DV>
-__global__ void __launch_bounds__(DV) decode_paged_join_kernel(const DecodeArgs<T> a) {
+__global__ void __launch_bounds__(256) decode_paged_join_kernel(const DecodeArgs<T> a) {
     griddep_sync();
-    const int h = blockIdx.x, b = blockIdx.y, col = threadIdx.x;
+    __shared__ float f[MAX_SPLITS], red[256], top[8], tot[8];
+    __shared__ int any_bad;
+    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     View w;
     view_of(a, b, &w);
     const int n = min(a.n_split, max(1, (w.n + a.split_keys - 1) / a.split_keys));
     const float* p = a.part + ((long long)b * a.H + h) * a.n_split * (DV + 4);
-    float m = -INFINITY;
-    for (int s = 0; s < n; ++s) m = fmaxf(m, p[s * (DV + 4) + DV]);
-    const float mu = m == -INFINITY ? 0.f : m;
-    float sum = 0.f, l = 0.f;
-    bool bad = false;
-    for (int s = 0; s < n; ++s) {
-        const float ls = p[s * (DV + 4) + DV + 1], f = exp2f(p[s * (DV + 4) + DV] - mu);
-        bad |= ls < 0.f;
-        l = fmaf(ls, f, l);
-        sum = fmaf(p[s * (DV + 4) + col], f, sum);
+    static_assert(MAX_SPLITS <= 256, "one split per thread");
+    const float m = tid < n ? p[tid * (DV + 4) + DV] : -INFINITY, ls = tid < n ? p[tid * (DV + 4) + DV + 1] : 0.f;
+    if (tid == 0) any_bad = 0;
+    float to = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+    if (lane == 0) top[warp] = to;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < 8; ++x) to = fmaxf(to, top[x]);
+    const float e = tid < n ? fast_exp2(m - (to == -INFINITY ? 0.f : to)) : 0.f;
+    if (ls < 0.f) any_bad = 1;
+    if (tid < n) f[tid] = e;
+    float l = ls * e;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) tot[warp] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) l += tot[x];
+    constexpr int NP = 256 / DV;
+    const int col = tid % DV, part = tid / DV;
+    float sum = 0.f;
+#pragma unroll 4
+    for (int s = part; s < n; s += NP) sum = fmaf(p[s * (DV + 4) + col], f[s], sum);
+    red[tid] = sum;
+    __syncthreads();
+    if (tid < DV) {
+#pragma unroll
+        for (int x = 1; x < NP; ++x) sum += red[x * DV + tid];
+        a.o[b * a.ldo + (long long)h * DV + tid] = from_f<T>(any_bad || l == 0.f ? 0.f : sum / l);
     }
-    a.o[b * a.ldo + (long long)h * DV + col] = from_f<T>(bad || l == 0.f ? 0.f : sum / l);
 }
 
 // How the keys are split: a function of the call's host arguments alone, so that the
-// workspace has one size. Splits of whole 128-key chunks, enough blocks to fill the GPU's
-// 148 SMs several times over.
+// workspace has one size. `units` (KV heads and groups of all sequences) are the blocks
+// without splitting, `slots` what the GPU's 148 SMs hold at a time.
+//   - Where all sequences see about equally many keys (a window that is full, or a short
+//     cache): up to 8 splits that still fit one wave; all blocks then share the bandwidth and
+//     finish together, and the splits join within a cluster. 64 sequences, window 1024: 25.7
+//     us in 1 split, 33.0 in 2 (a wave and a half); 16 of them: 10.8 in 4 with a cluster, 11.5
+//     with the join kernel; one sequence of 1153: 5.8 in 7 against 6.3 in 10 with the join.
+//   - Where the lengths may differ much (a global layer's long cache): about 8 blocks per SM,
+//     which spread over the SMs as they come free, joined by the kernel after. 64 sequences of
+//     up to 4224: 63.1 us in 4 splits, 71.8 in 1 (clusters of 4: 72.0, they wait for room); 16
+//     of up to 32896: 101 in 15, 150 in 4. More than 64 splits of one sequence cost more in
+//     the join than they give (one of 32000: 18.7 us in 60, 25.5 in 118).
 struct Split {
     int keys, n;
+    bool cluster;
 };
 int heads_per_block(const hymba_attn_shape& s) {
     return s.dtype == HYMBA_F32 || s.n_q_heads / s.n_kv_heads <= 8 ? 8 : 16;
 }
 Split split_of(const hymba_attn_shape& s, int batch, int max_len) {
-    const long long span = s.window > 0 ? std::min<long long>(max_len, (long long)s.n_meta + s.window) : max_len;
+    const long long full = (long long)s.n_meta + s.window;
+    const bool windowed = s.window > 0 && full <= max_len;
+    const long long span = windowed ? full : max_len;
     const int R = s.n_q_heads / s.n_kv_heads, hb = heads_per_block(s);
     const long long units = (long long)batch * s.n_kv_heads * ((R + hb - 1) / hb);
-    const long long chunks = (span + SC - 1) / SC;
-    const long long want = std::max<long long>(1, std::min(chunks, (148 * 8 + units - 1) / units));
+    const int step = s.dtype == HYMBA_F32 ? SC : 4 * TK;
+    const long long chunks = (span + step - 1) / step;
+    const long long slots = 148 * blocks_per_sm(s.head_dim + s.v_head_dim, hb / 8);
+    const bool even = s.dtype != HYMBA_F32 && (span <= 1536 || (windowed && (span <= 4096 || units > slots / MAX_CL)));
+    const long long most = even ? std::min<long long>(MAX_CL, slots / units) : std::min<long long>(MAX_SPLITS, (148 * 8 + units - 1) / units);
+    const long long want = std::max<long long>(1, std::min(chunks, most));
     Split r;
-    r.keys = (int)((chunks + want - 1) / want) * SC;
+    r.keys = (int)((chunks + want - 1) / want) * step;
     r.n = (int)((span + r.keys - 1) / r.keys);
+    r.cluster = even && r.n > 1;
     return r;
 }
 
 template <typename T, int DH, int DV, int NG>
-int launch_decode_mma(const Ctx& ctx, const DecodeArgs<T>& a, int batch) {
+int launch_decode_mma(const Ctx& ctx, const DecodeArgs<T>& a, int batch, bool cluster) {
     const int R = a.H / a.G;
-    auto kern = decode_paged_mma_kernel<T, DH, DV, NG>;
-    const size_t smem = 4 * RING;
-    static std::atomic<unsigned long long> smem_set{0};
-    if (!smem_opt_in_once(smem_set, kern, smem, ctx)) return HYMBA_ERR_CUDA;
-    dim3 grid(a.n_split, a.G * ((R + 8 * NG - 1) / (8 * NG)), batch);
-    HYMBA_LAUNCH(ctx, "attn_decode_paged", kern, grid, 128, smem, a, ctx.status);
+    const size_t smem = 4 * Ring<DH, DV>::SIZE;
+    const dim3 grid(a.n_split, a.G * ((R + 8 * NG - 1) / (8 * NG)), batch);
+    static std::atomic<unsigned long long> smem_set[2];
+    if (cluster) {
+        auto kern = decode_paged_mma_kernel<T, DH, DV, NG, true>;
+        if (!smem_opt_in_once(smem_set[1], kern, smem, ctx)) return HYMBA_ERR_CUDA;
+        HYMBA_LAUNCH_CLUSTER(ctx, "attn_decode_paged", kern, grid, 128, smem, (unsigned)a.n_split, a, ctx.status);
+    } else {
+        auto kern = decode_paged_mma_kernel<T, DH, DV, NG, false>;
+        if (!smem_opt_in_once(smem_set[0], kern, smem, ctx)) return HYMBA_ERR_CUDA;
+        HYMBA_LAUNCH(ctx, "attn_decode_paged", kern, grid, 128, smem, a, ctx.status);
+    }
     return HYMBA_OK;
 }
 
 template <typename T, int DH, int DV>
-int launch_decode_dims(const Ctx& ctx, const DecodeArgs<T>& a, int batch) {
+int launch_decode_dims(const Ctx& ctx, const DecodeArgs<T>& a, int batch, bool cluster) {
     const int R = a.H / a.G;
     if constexpr (sizeof(T) == 2) {
-        const int rc = R <= 8 ? launch_decode_mma<T, DH, DV, 1>(ctx, a, batch) : launch_decode_mma<T, DH, DV, 2>(ctx, a, batch);
+        const int rc = R <= 8 ? launch_decode_mma<T, DH, DV, 1>(ctx, a, batch, cluster)
+                              : launch_decode_mma<T, DH, DV, 2>(ctx, a, batch, cluster);
         if (rc) return rc;
     } else {
         dim3 grid(a.n_split, a.G * ((R + SR - 1) / SR), batch);
         HYMBA_LAUNCH(ctx, "attn_decode_paged", (decode_paged_simt_kernel<T, DH, DV>), grid, 128, 0, a, ctx.status);
     }
-    if (a.n_split > 1)
-        HYMBA_LAUNCH(ctx, "attn_decode_paged_join", (decode_paged_join_kernel<T, DV>), dim3(a.H, batch), DV, 0, a);
+    if (a.n_split > 1 && !cluster)
+        HYMBA_LAUNCH(ctx, "attn_decode_paged_join", (decode_paged_join_kernel<T, DV>), dim3(a.H, batch), 256, 0, a);
     return HYMBA_OK;
 }
 
@@ -579,10 +706,10 @@ int launch_decode_type(const Ctx& ctx, const hymba_attn_shape& s, float scale, c
     a.split_keys = sp.keys;
     a.n_split = sp.n;
     a.scale_log2 = scale * LOG2E;
-    if (s.head_dim == 64 && s.v_head_dim == 64) return launch_decode_dims<T, 64, 64>(ctx, a, kv.batch);
-    if (s.head_dim == 64 && s.v_head_dim == 128) return launch_decode_dims<T, 64, 128>(ctx, a, kv.batch);
-    if (s.head_dim == 128 && s.v_head_dim == 64) return launch_decode_dims<T, 128, 64>(ctx, a, kv.batch);
-    if (s.head_dim == 128 && s.v_head_dim == 128) return launch_decode_dims<T, 128, 128>(ctx, a, kv.batch);
+    if (s.head_dim == 64 && s.v_head_dim == 64) return launch_decode_dims<T, 64, 64>(ctx, a, kv.batch, sp.cluster);
+    if (s.head_dim == 64 && s.v_head_dim == 128) return launch_decode_dims<T, 64, 128>(ctx, a, kv.batch, sp.cluster);
+    if (s.head_dim == 128 && s.v_head_dim == 64) return launch_decode_dims<T, 128, 64>(ctx, a, kv.batch, sp.cluster);
+    if (s.head_dim == 128 && s.v_head_dim == 128) return launch_decode_dims<T, 128, 128>(ctx, a, kv.batch, sp.cluster);
     return HYMBA_ERR_UNSUPPORTED;
 }
 
@@ -609,13 +736,15 @@ int launch_kv_append(const Ctx& ctx, const hymba_paged_kv& kv, int esz, const vo
     a.kshift = a.vshift = 0;
     while ((16 << a.kshift) < kv.head_dim * esz) ++a.kshift;
     while ((16 << a.vshift) < kv.v_head_dim * esz) ++a.vshift;
-    HYMBA_LAUNCH(ctx, "kv_append_paged", kv_append_kernel, ceil_div(rows, 8), 256, 0, a, ctx.status);
+    // one row per warp while that leaves warps free, eight rows once the GPU is full of them
+    if (rows < 148 * 64) HYMBA_LAUNCH(ctx, "kv_append_paged", kv_append_kernel<1>, ceil_div(rows, 8), 256, 0, a, ctx.status);
+    else HYMBA_LAUNCH(ctx, "kv_append_paged", kv_append_kernel<8>, ceil_div(rows, 64), 256, 0, a, ctx.status);
     return HYMBA_OK;
 }
 
 size_t decode_paged_bytes(const hymba_attn_shape& s, int batch, int max_len) {
     const Split sp = split_of(s, batch, max_len);
-    if (sp.n == 1) return 256;
+    if (sp.n == 1 || sp.cluster) return 256;
     return (size_t)round_up((long long)batch * s.n_q_heads * sp.n * (s.v_head_dim + 4) * 4, 256);
 }
 

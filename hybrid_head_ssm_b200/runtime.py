@@ -141,6 +141,11 @@ def mlp(m: DeviceMLP, h: torch.Tensor, ws: torch.Tensor) -> None:
 # ragged batches: packed prompts, paged K/V, linear attention
 # ---------------------------------------------------------------------------
 TORCH_DTYPE = {HYMBA_F16: torch.float16, HYMBA_BF16: torch.bfloat16, HYMBA_F32: torch.float32}
+_DTYPE_CODE = {v: k for k, v in TORCH_DTYPE.items()}
+_F32, _I32 = torch.float32, torch.int32
+# the current stream's handle without building a Stream object (2 us of the smallest calls)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _need(ok: bool, what: str) -> None:
@@ -148,39 +153,46 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _rows(name: str, t: torch.Tensor, width: int, code: int, dev: torch.device) -> int:
+def _misfit(name: str, t: torch.Tensor, what: str) -> ValueError:
+    return ValueError(f"{name}: {what} wanted, got {tuple(t.shape)} with strides {t.stride()} of {t.dtype} on {t.device}")
+
+
+def _rows(name: str, t: torch.Tensor, rows: int, width: int, dtype: torch.dtype, dev: torch.device) -> int:
     """Row stride of a [rows, width] tensor of one type on one device, its elements side by
     side within a row."""
-    if t.dim() != 2 or t.shape[1] != width or t.dtype is not TORCH_DTYPE.get(code) or t.device != dev:
-        raise ValueError(f"{name}: [rows, {width}] of {TORCH_DTYPE.get(code)} on {dev} wanted, got "
-                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
-    if width > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the elements of a row must lie side by side")
+    if t.shape != (rows, width) or t.dtype is not dtype or t.device != dev:
+        raise _misfit(name, t, f"[{rows}, {width}] of {dtype} on {dev}")
+    ld, step = t.stride()
+    if step != 1 and width > 1:
+        raise _misfit(name, t, "elements side by side within a row")
     # the stride of a single row is never used (and torch may report anything for it)
-    return t.stride(0) if t.shape[0] > 1 else width
+    return ld if rows > 1 else width
 
 
-def _ints(name: str, t: torch.Tensor, shape, dev: torch.device) -> None:
-    if t.dtype is not torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != dev:
-        raise ValueError(f"{name}: contiguous int32 {tuple(shape)} on {dev} wanted, got {tuple(t.shape)} of "
-                         f"{t.dtype} on {t.device}")
+def _dense(name: str, t: torch.Tensor, shape, dtype: torch.dtype, dev: torch.device) -> None:
+    if t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        raise _misfit(name, t, f"contiguous {tuple(shape)} of {dtype} on {dev}")
 
 
-def _floats(name: str, t: torch.Tensor, shape, dev: torch.device) -> None:
-    if t.dtype is not torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != dev:
-        raise ValueError(f"{name}: contiguous float32 {tuple(shape)} on {dev} wanted, got {tuple(t.shape)} of "
-                         f"{t.dtype} on {t.device}")
+def _scratch(ws: torch.Tensor, dev: torch.device) -> int:
+    if ws.device != dev or not ws.is_contiguous():
+        raise _misfit("workspace", ws, f"a contiguous tensor on {dev}")
+    return ws.numel() * ws.element_size()
 
 
 def _queue(dev: torch.device, fn, *args) -> None:
     """Call fn(*args, stream) with the tensors' device current, on torch's current stream
     of that device."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
-        check(fn(*args, stream))
+    if dev.type != "cuda":
+        raise ValueError(f"tensors on a CUDA device wanted, got {dev}")
+    index = dev.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            check(fn(*args, stream))
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc:
+        check(rc)
 
 
 class PagedKV:
@@ -189,21 +201,20 @@ class PagedKV:
     [batch]; the tensors stay the caller's and are kept alive here."""
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, length: torch.Tensor):
-        code = {v: k for k, v in TORCH_DTYPE.items()}.get(k_pages.dtype)
-        dev = k_pages.device
-        _need(code is not None and k_pages.dim() == 4 and k_pages.is_contiguous(),
-              "k_pages: contiguous [n_pages, n_kv_heads, page_size, head_dim] of float16, bfloat16 or float32")
-        _need(v_pages.dim() == 4 and v_pages.is_contiguous() and v_pages.shape[:3] == k_pages.shape[:3]
-              and v_pages.dtype is k_pages.dtype and v_pages.device == dev,
-              "v_pages: contiguous, with k_pages' pages, heads, page size, type and device")
-        _need(page_table.dim() == 2, "page_table: [batch, max_pages]")
-        _ints("page_table", page_table, page_table.shape, dev)
-        _ints("len", length, (page_table.shape[0],), dev)
-        self.k_pages, self.v_pages, self.page_table, self.len = k_pages, v_pages, page_table, length
-        self.device = dev
+        code, dev = _DTYPE_CODE.get(k_pages.dtype), k_pages.device
+        if code is None or k_pages.dim() != 4 or not k_pages.is_contiguous():
+            raise _misfit("k_pages", k_pages, "contiguous [n_pages, n_kv_heads, page_size, head_dim] of float16, "
+                          "bfloat16 or float32")
         n_pages, G, page, dh = k_pages.shape
+        _need(v_pages.dim() == 4 and page_table.dim() == 2, "v_pages of 4 dimensions, page_table [batch, max_pages]")
+        _dense("v_pages", v_pages, (n_pages, G, page, v_pages.shape[3]), k_pages.dtype, dev)
+        _dense("page_table", page_table, page_table.shape, _I32, dev)
+        _dense("len", length, (page_table.shape[0],), _I32, dev)
+        self.k_pages, self.v_pages, self.page_table, self.len = k_pages, v_pages, page_table, length
+        self.device, self.dtype, self.batch = dev, k_pages.dtype, page_table.shape[0]
+        self.k_width, self.v_width = G * dh, G * v_pages.shape[3]
         self.s = hymba_paged_kv(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), length.data_ptr(),
-                                n_pages, page, page_table.shape[1], page_table.shape[0], G, dh, v_pages.shape[3], code)
+                                n_pages, page, page_table.shape[1], self.batch, G, dh, v_pages.shape[3], code)
         self.ref = ctypes.byref(self.s)
 
 
@@ -211,26 +222,25 @@ def attn_prefill_packed(shape, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
                         o: torch.Tensor) -> None:
     """o [rows, H * dv] = causal attention of the packed prompts q [rows, H * dh], k [rows,
     G * dh], v [rows, G * dv]; cu_seqlens int32 [sequences + 1]."""
-    s, dev, rows = shape, q.device, q.shape[0]
-    lds = [_rows(n, t, w, s.dtype, dev) for n, t, w in (
-        ("q", q, s.n_q_heads * s.head_dim), ("k", k, s.n_kv_heads * s.head_dim), ("v", v, s.n_kv_heads * s.v_head_dim),
-        ("o", o, s.n_q_heads * s.v_head_dim))]
-    _need(k.shape[0] == rows and v.shape[0] == rows and o.shape[0] == rows, "q, k, v and o: as many rows")
-    _ints("cu_seqlens", cu_seqlens, (cu_seqlens.numel(),), dev)
-    _queue(dev, hymba_attn_prefill_packed, ctypes.byref(s), q.data_ptr(), lds[0], k.data_ptr(), lds[1], v.data_ptr(),
-           lds[2], cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, rows, o.data_ptr(), lds[3])
+    H, G, dh, dv = shape.n_q_heads, shape.n_kv_heads, shape.head_dim, shape.v_head_dim
+    rows, dev, dtype = q.shape[0], q.device, TORCH_DTYPE.get(shape.dtype)
+    ldq, ldk = _rows("q", q, rows, H * dh, dtype, dev), _rows("k", k, rows, G * dh, dtype, dev)
+    ldv, ldo = _rows("v", v, rows, G * dv, dtype, dev), _rows("o", o, rows, H * dv, dtype, dev)
+    n = cu_seqlens.numel()
+    _dense("cu_seqlens", cu_seqlens, (n,), _I32, dev)
+    _queue(dev, hymba_attn_prefill_packed, ctypes.byref(shape), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(),
+           ldv, cu_seqlens.data_ptr(), n - 1, rows, o.data_ptr(), ldo)
 
 
 def kv_append_paged(kv: PagedKV, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None) -> None:
     """The rows of k [rows, G * dh] and v [rows, G * dv] become their sequences' newest
     positions (kv.len counts them already); cu_seqlens None: one row per sequence."""
-    s, dev = kv.s, kv.device
-    ldk, ldv = _rows("k", k, s.n_kv_heads * s.head_dim, s.dtype, dev), _rows("v", v, s.n_kv_heads * s.v_head_dim, s.dtype, dev)
-    _need(k.shape[0] == v.shape[0], "k and v: as many rows")
+    rows, dev, cu = k.shape[0], kv.device, None
+    ldk, ldv = _rows("k", k, rows, kv.k_width, kv.dtype, dev), _rows("v", v, rows, kv.v_width, kv.dtype, dev)
     if cu_seqlens is not None:
-        _ints("cu_seqlens", cu_seqlens, (s.batch + 1,), dev)
-    _queue(dev, hymba_kv_append_paged, kv.ref, k.data_ptr(), ldk, v.data_ptr(), ldv,
-           None if cu_seqlens is None else cu_seqlens.data_ptr(), k.shape[0])
+        _dense("cu_seqlens", cu_seqlens, (kv.batch + 1,), _I32, dev)
+        cu = cu_seqlens.data_ptr()
+    _queue(dev, hymba_kv_append_paged, kv.ref, k.data_ptr(), ldk, v.data_ptr(), ldv, cu, rows)
 
 
 def decode_paged_workspace(shape, batch: int, max_len: int, device="cuda") -> torch.Tensor:
@@ -243,29 +253,23 @@ def attn_decode_paged(shape, q: torch.Tensor, kv: PagedKV, o: torch.Tensor, ws: 
     """o [batch, H * dv] = attention of the newest position of every sequence (q [batch, H *
     dh]) over its pages. max_len: a bound on every length (0: the page table's capacity);
     ws from decode_paged_workspace with that bound."""
-    s, dev = shape, kv.device
-    ldq, ldo = _rows("q", q, s.n_q_heads * s.head_dim, s.dtype, dev), _rows("o", o, s.n_q_heads * s.v_head_dim, s.dtype, dev)
-    _need(q.shape[0] == kv.s.batch and o.shape[0] == kv.s.batch, "q and o: one row per sequence")
-    _need(ws.device == dev and ws.is_contiguous(), "workspace: contiguous, on the cache's device")
-    _queue(dev, hymba_attn_decode_paged, ctypes.byref(s), q.data_ptr(), ldq, kv.ref, max_len, o.data_ptr(), ldo,
-           ws.data_ptr(), ws.numel() * ws.element_size())
+    H, dev = shape.n_q_heads, kv.device
+    ldq = _rows("q", q, kv.batch, H * shape.head_dim, kv.dtype, dev)
+    ldo = _rows("o", o, kv.batch, H * shape.v_head_dim, kv.dtype, dev)
+    _queue(dev, hymba_attn_decode_paged, ctypes.byref(shape), q.data_ptr(), ldq, kv.ref, max_len, o.data_ptr(), ldo,
+           ws.data_ptr(), _scratch(ws, dev))
 
 
-def _linear_rows(s, q, k, v, g, o, dev):
-    rows = q.shape[0]
-    lds = [_rows(n, t, w, s.dtype, dev) for n, t, w in (
-        ("q", q, s.n_qk_heads * s.key_dim), ("k", k, s.n_qk_heads * s.key_dim), ("v", v, s.n_heads * s.v_head_dim),
-        ("o", o, s.n_heads * s.v_head_dim))]
-    _need(k.shape[0] == rows and v.shape[0] == rows and o.shape[0] == rows, "q, k, v and o: as many rows")
+def _decays(g: torch.Tensor, rows: int, heads: int, dev: torch.device) -> int:
+    """Row stride of the log decays: float32 [rows, heads], or [heads] (0: the same for every
+    row, as for rows expanded from one)."""
     if g.dim() == 1:
-        # one decay per head for every row
-        _floats("g", g, (s.n_heads,), dev)
-        return lds, 0
-    _need(g.shape[0] == rows, "g: [n_heads], or [rows, n_heads]")
-    if rows > 1 and g.stride(0) == 0:
-        _rows("g", g[:1], s.n_heads, HYMBA_F32, dev)
-        return lds, 0
-    return lds, _rows("g", g, s.n_heads, HYMBA_F32, dev)
+        _dense("g", g, (heads,), _F32, dev)
+        return 0
+    if rows > 1 and g.stride(0) == 0 and g.shape[0] == rows:
+        _rows("g", g[:1], 1, heads, _F32, dev)
+        return 0
+    return _rows("g", g, rows, heads, _F32, dev)
 
 
 def linattn_workspace(shape, n_seqs: int, rows: int, device="cuda") -> torch.Tensor:
@@ -280,26 +284,32 @@ def linattn_prefill(shape, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g:
     """o [rows, H * dv] of the packed prompts q, k [rows, Hk * dk], v [rows, H * dv] with log
     decays g float32 [rows, H] or [H]; states float32 [sequences, H, dv, dk] before and
     after the prompts."""
-    s, dev = shape, q.device
-    lds, ldg = _linear_rows(s, q, k, v, g, o, dev)
-    _ints("cu_seqlens", cu_seqlens, (cu_seqlens.numel(),), dev)
+    Hk, H, dk, dv = shape.n_qk_heads, shape.n_heads, shape.key_dim, shape.v_head_dim
+    rows, dev, dtype = q.shape[0], q.device, TORCH_DTYPE.get(shape.dtype)
+    ldq, ldk = _rows("q", q, rows, Hk * dk, dtype, dev), _rows("k", k, rows, Hk * dk, dtype, dev)
+    ldv, ldo = _rows("v", v, rows, H * dv, dtype, dev), _rows("o", o, rows, H * dv, dtype, dev)
     n = cu_seqlens.numel() - 1
-    for name, t in (("state_in", state_in), ("state_out", state_out)):
-        if t is not None:
-            _floats(name, t, (n, s.n_heads, s.v_head_dim, s.key_dim), dev)
-    _need(ws.device == dev and ws.is_contiguous(), "workspace: contiguous, on the rows' device")
-    _queue(dev, hymba_linattn_prefill, ctypes.byref(s), q.data_ptr(), lds[0], k.data_ptr(), lds[1], v.data_ptr(),
-           lds[2], g.data_ptr(), ldg, cu_seqlens.data_ptr(), n, q.shape[0],
-           None if state_in is None else state_in.data_ptr(), None if state_out is None else state_out.data_ptr(),
-           o.data_ptr(), lds[3], ws.data_ptr(), ws.numel() * ws.element_size())
+    _dense("cu_seqlens", cu_seqlens, (n + 1,), _I32, dev)
+    first = last = None
+    if state_in is not None:
+        _dense("state_in", state_in, (n, H, dv, dk), _F32, dev)
+        first = state_in.data_ptr()
+    if state_out is not None:
+        _dense("state_out", state_out, (n, H, dv, dk), _F32, dev)
+        last = state_out.data_ptr()
+    _queue(dev, hymba_linattn_prefill, ctypes.byref(shape), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+           g.data_ptr(), _decays(g, rows, H, dev), cu_seqlens.data_ptr(), n, rows, first, last, o.data_ptr(), ldo,
+           ws.data_ptr(), _scratch(ws, dev))
 
 
 def linattn_step(shape, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
                  o: torch.Tensor) -> None:
     """One token per sequence: state float32 [batch, H, dv, dk] is updated in place, o [batch,
     H * dv] is its product with the token's query."""
-    s, dev = shape, q.device
-    lds, ldg = _linear_rows(s, q, k, v, g, o, dev)
-    _floats("state", state, (q.shape[0], s.n_heads, s.v_head_dim, s.key_dim), dev)
-    _queue(dev, hymba_linattn_step, ctypes.byref(s), q.data_ptr(), lds[0], k.data_ptr(), lds[1], v.data_ptr(), lds[2],
-           g.data_ptr(), ldg, state.data_ptr(), q.shape[0], o.data_ptr(), lds[3])
+    Hk, H, dk, dv = shape.n_qk_heads, shape.n_heads, shape.key_dim, shape.v_head_dim
+    rows, dev, dtype = q.shape[0], q.device, TORCH_DTYPE.get(shape.dtype)
+    ldq, ldk = _rows("q", q, rows, Hk * dk, dtype, dev), _rows("k", k, rows, Hk * dk, dtype, dev)
+    ldv, ldo = _rows("v", v, rows, H * dv, dtype, dev), _rows("o", o, rows, H * dv, dtype, dev)
+    _dense("state", state, (rows, H, dv, dk), _F32, dev)
+    _queue(dev, hymba_linattn_step, ctypes.byref(shape), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+           g.data_ptr(), _decays(g, rows, H, dev), state.data_ptr(), rows, o.data_ptr(), ldo)

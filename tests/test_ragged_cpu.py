@@ -300,6 +300,14 @@ def test_helpers_refuse_tensors_that_do_not_fit(hy):
             rt.linattn_prefill(ls, lq, lq, lv, a["g"], cu, lo, ws, a["st"])
     with pytest.raises(ValueError):
         rt.linattn_step(ls, lq, lq, lv, g, st, lo)
+    # tensors that fit, but not on a GPU: never handed to a kernel
+    table[:] = 1
+    for call in (lambda: rt.attn_prefill_packed(s, q, k, v, cu, o), lambda: rt.kv_append_paged(kv, k, v, cu),
+                 lambda: rt.attn_decode_paged(s, q[:2], kv, o[:2], ws),
+                 lambda: rt.linattn_prefill(ls, lq, lq, lv, g, cu, lo, ws, st, st),
+                 lambda: rt.linattn_step(ls, lq[:2], lq[:2], lv[:2], g[:2], st, lo[:2])):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
 
 
 def test_workload_shapes_are_accepted(hy):
