@@ -174,5 +174,9 @@ int launch_linattn_recurrent(const Ctx& ctx, const LinAttn& a);
 // Packed prompts of 16-bit rows in chunks of 64 rows, tensor cores.
 template <typename T>
 int launch_linattn_chunk(const Ctx& ctx, const LinAttn& a);
+// The same in chunks of 128 rows on the tcgen05 tensor cores, for key dim 64.
+bool linattn_tc_applies(const LinAttn& a);
+template <typename T>
+int launch_linattn_tc(const Ctx& ctx, const LinAttn& a);
 
 }  // namespace hymba

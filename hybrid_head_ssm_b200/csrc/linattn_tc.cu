@@ -1,0 +1,740 @@
+// Linear attention with a decay per head, chunked form on the tcgen05 tensor cores (16-bit
+// rows, key dim 64): S_t = exp(g_t) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t over packed
+// prompts ("Lecture 04 - Beyond the Dense Transformer", section 3: with a scalar decay per
+// head the recurrence is a masked product with a semiseparable matrix and can be computed as
+// blocks of matmuls). Per chunk of 128 rows, with cs_i = g_1 + .. + g_i from the chunk's start:
+//     o_i = scale (sum_{j<=i} exp(cs_i - cs_j) (q_i . k_j) v_j  +  exp(cs_i) S q_i)
+//     S  <- exp(cs_128) S + sum_j exp(cs_128 - cs_j) v_j k_j^T
+//
+// One CTA per (64 or 128 value columns, head, sequence) walks the chunks. 12 warps:
+//   warp 0      TMA of q, k, v, two chunks deep;
+//   warp 1      TMEM, and one thread that issues the four products of a chunk:
+//               S1 = q k^T (128 x 128 x 64), D += V^T K' (the state, values x keys, both
+//               operands read across their rows), O2 = q S^T, O = P V (P from TMEM over S1);
+//   warp 2      the decay tables of the next chunk from 64-bit sums;
+//   warp 3      V: rows behind the sequence become zero, values that are not finite are noted;
+//   warps 4-7   one thread per row i: P = mask * decay * scale * S1 as 16-bit pairs into TMEM,
+//               then o_i = O + exp(cs_i) scale O2 to global memory;
+//   warps 8-11  one thread per state row (value) and chunk row: the state from TMEM, its
+//               16-bit copy for O2 to shared memory, the decayed state back; then K' = exp(cs_128 -
+//               cs_j) k_j as 16-bit parts in shared memory.
+// The chains of the two warpgroups overlap: while P and o of a chunk are formed, the state
+// group prepares the products of the same chunk, and S1 of the next follows the last read of P.
+//
+// Numbers: a decay between rows of different 32-row blocks is A_i B_j, both distances from
+// the start of i's block and so at most 1 each (a chunk with a positive log decay forms
+// 2^(a_i + b_j) instead), within a block 2^(a_i + b_j). K' enters as three parts (bf16) or two
+// (fp16), at least 22 bits of every term of the fp32 state; P and the state's copy are rounded
+// to the rows' type, like any MMA operand. fp16 has little range: P's rows, the copy's rows and
+// K' are brought to the middle of it by powers of two that the fp32 values give back (the
+// state in TMEM carries K's power, changed together with its decay).
+// A CTA that noted a value of V that is not finite computes its sequence once more by the
+// recurrence, in which nothing reaches a row that does not see it.
+// Bound: HBM (q, k, v read and o written once per 128 value columns).
+#include "attn_tile.cuh"
+#include "kernels.h"
+#include "ragged.cuh"
+
+namespace hymba {
+
+namespace {
+
+constexpr int CQ = 128;  // rows per chunk
+constexpr int DK = 64;
+constexpr int NT = 384;
+constexpr int TILE = CQ * 128;  // bytes of 128 rows x 64 16-bit columns
+// TMEM columns: S1 / P, O, O2, the state
+constexpr uint32_t TM_S1 = 0, TM_O = 128, TM_O2 = 256, TM_D = 384;
+
+// Per chunk, from its log decays (log2 units; cs_i the inclusive sums):
+struct Tables {
+    alignas(16) float a[CQ];       // cs_i - cs at the start of i's 32-row block + log2 scale
+    alignas(16) float b[CQ];       // cs at the start of j's block - cs_j
+    alignas(16) float B[3][96];    // 2^(cs at the start of block t + 1 - cs_j), j below that block
+    alignas(16) float e[CQ];       // 2^cs_i scale
+    alignas(16) float w[CQ];       // 2^(cs_127 - cs_j); 0 behind the sequence
+    float between[4][4];           // cs at the start of block t - cs at the start of block u
+    float dec;                     // 2^cs_127
+    int resets;                    // a decay within the chunk may be 0
+    int grows;                     // a log decay is positive
+};
+
+template <int PARTS>
+struct TcSmem {
+    alignas(1024) uint8_t q[2][TILE];
+    alignas(1024) uint8_t k[2][TILE];
+    alignas(1024) uint8_t v[2][2][TILE];
+    alignas(1024) uint8_t ks[PARTS][TILE];  // K' parts, rows j
+    alignas(1024) uint8_t s16[2][TILE];     // the state's copy, rows = values
+    Tables tab[2];
+    float col[2][CQ];  // fp16: 1 / power of two of the copy's rows
+    float kmax[2][4];
+    uint64_t full[2], empty[2], v_ok[2], tab_full[2], tab_empty[2];
+    uint64_t s1_full, p_full, o_full, o_free, s_ready, k_ready, k_max, d_done, drain;
+    uint32_t tmem_base;
+    int abort, dirty;
+};
+
+struct Args {
+    const void *q, *k, *v;
+    void* o;
+    long long ldq, ldk, ldv, ldo, ldg;
+    const float *g, *state_in;
+    float* state_out;
+    const int* cu;
+    int total, Hk, H, dv;
+    float log2_scale;
+};
+
+__device__ __forceinline__ void fail(volatile int* abort, int* status, int role, int step, int bar) {
+    *abort = 1;
+    tc::record_timeout(status, role, step, bar);
+}
+
+// a power of two that brings x (> 0) near 2^12, within 2^low and 2^high; 1 for 0 and what is
+// not finite
+__device__ __forceinline__ float to_middle(float x, int low, int high) {
+    const int e = (__float_as_int(x) >> 23) & 255;
+    if (e == 0 || e == 255) return 1.f;
+    return __int_as_float((127 + min(max(127 - e + 12, low), high)) << 23);
+}
+// the inverse of a power of two: its exponent mirrored
+__device__ __forceinline__ float inverse(float p) { return __int_as_float(0x7f000000 - __float_as_int(p)); }
+// a decay of 0 drops what it multiplies, also what is not finite
+__device__ __forceinline__ float fade(float d, float x) { return d == 0.f ? 0.f : d * x; }
+
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    const T* x = reinterpret_cast<const T*>(&w);
+    return make_float2(to_f(x[0]), to_f(x[1]));
+}
+
+// the tables of one chunk; lane l holds the log decays of rows 4 l .. 4 l + 3; n rows are real
+__device__ __forceinline__ void make_tables(Tables& t, const float (&g)[4], int n, float lsc) {
+    constexpr double LOG2E = 1.4426950408889634;
+    const int lane = threadIdx.x & 31, blk = lane >> 3;
+    double d[4], x[4];
+    float down = 0.f;
+    bool up = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        d[i] = (double)g[i] * LOG2E;
+        // a decay below 2^-160 is 0 in fp32; the limit keeps -infinity out of the sums
+        if (d[i] < -160.0) d[i] = -160.0;
+        down += fminf((float)d[i], 0.f);
+        up |= !(d[i] <= 0.0);
+    }
+    double sum = (d[0] + d[1]) + (d[2] + d[3]);
+    const double own = sum;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, sum, w);
+        if (lane >= w) sum += y;
+    }
+    const double last = __shfl_sync(0xffffffffu, sum, 31);
+    double c[4] = {0.0, __shfl_sync(0xffffffffu, sum, 7), __shfl_sync(0xffffffffu, sum, 15),
+                   __shfl_sync(0xffffffffu, sum, 23)};
+    const double from = blk == 0 ? c[0] : blk == 1 ? c[1] : blk == 2 ? c[2] : c[3];
+    double before = __shfl_up_sync(0xffffffffu, sum, 1);
+    if (lane == 0) before = 0.0;
+    (void)own;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        before += d[i];
+        x[i] = before;
+    }
+    float va[4], vb[4], ve[4], vw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        va[i] = (float)(x[i] - from) + lsc;
+        vb[i] = (float)(from - x[i]);
+        ve[i] = fast_exp2((float)x[i] + lsc);
+        vw[i] = 4 * lane + i < n ? fast_exp2((float)(last - x[i])) : 0.f;
+    }
+    *reinterpret_cast<float4*>(&t.a[4 * lane]) = make_float4(va[0], va[1], va[2], va[3]);
+    *reinterpret_cast<float4*>(&t.b[4 * lane]) = make_float4(vb[0], vb[1], vb[2], vb[3]);
+    *reinterpret_cast<float4*>(&t.e[4 * lane]) = make_float4(ve[0], ve[1], ve[2], ve[3]);
+    *reinterpret_cast<float4*>(&t.w[4 * lane]) = make_float4(vw[0], vw[1], vw[2], vw[3]);
+#pragma unroll
+    for (int b = 1; b < 4; ++b)
+        if (blk < b)
+            *reinterpret_cast<float4*>(&t.B[b - 1][4 * lane]) =
+                make_float4(fast_exp2((float)(c[b] - x[0])), fast_exp2((float)(c[b] - x[1])),
+                            fast_exp2((float)(c[b] - x[2])), fast_exp2((float)(c[b] - x[3])));
+    if (lane < 16) {
+        const int r = lane >> 2, u = lane & 3;
+        const double cr = r == 0 ? c[0] : r == 1 ? c[1] : r == 2 ? c[2] : c[3];
+        const double cu = u == 0 ? c[0] : u == 1 ? c[1] : u == 2 ? c[2] : c[3];
+        t.between[r][u] = (float)(cr - cu);
+    }
+    up = __any_sync(0xffffffffu, up);
+#pragma unroll
+    for (int w = 16; w; w >>= 1) down += __shfl_xor_sync(0xffffffffu, down, w);
+    if (lane == 0) {
+        t.dec = fast_exp2((float)last);
+        t.resets = !(down + fminf(lsc, 0.f) > -120.f);
+        t.grows = up;
+    }
+}
+
+// One value column of a sequence by the recurrence.
+template <typename T>
+__device__ __noinline__ void recurrence(const Args& a, int s, int h, int start, int len, int col) {
+    const int hk = h / (a.H / a.Hk);
+    const T* q = static_cast<const T*>(a.q) + start * a.ldq + (long long)hk * DK;
+    const T* k = static_cast<const T*>(a.k) + start * a.ldk + (long long)hk * DK;
+    const T* v = static_cast<const T*>(a.v) + start * a.ldv + (long long)h * a.dv + col;
+    T* o = static_cast<T*>(a.o) + start * a.ldo + (long long)h * a.dv + col;
+    const float* g = a.g + start * a.ldg + h;
+    const long long at = (((long long)s * a.H + h) * a.dv + col) * DK;
+    const float scale = exp2f(a.log2_scale);
+    float S[DK];
+#pragma unroll
+    for (int e = 0; e < DK; ++e) S[e] = a.state_in ? a.state_in[at + e] : 0.f;
+#pragma unroll 1
+    for (int t = 0; t < len; ++t) {
+        const float dec = expf(g[t * a.ldg]), x = to_f(v[t * a.ldv]);
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < DK; ++e) {
+            S[e] = fmaf(x, to_f(k[t * a.ldk + e]), fade(dec, S[e]));
+            sum = fmaf(S[e], to_f(q[t * a.ldq + e]), sum);
+        }
+        o[t * a.ldo] = from_f<T>(sum * scale);
+    }
+    if (a.state_out)
+#pragma unroll
+        for (int e = 0; e < DK; ++e) a.state_out[at + e] = S[e];
+}
+
+// 32 lanes x 32 columns of fp32, read
+__device__ __forceinline__ void ld32(uint32_t addr, float (&x)[32]) {
+    tc::tmem_ld32(addr, *reinterpret_cast<uint32_t(*)[32]>(&x));
+}
+
+template <typename T, int DV>
+__global__ void __launch_bounds__(NT, 1)
+linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const Args a, int* status) {
+    constexpr bool F16 = std::is_same<T, f16>::value;
+    constexpr int PARTS = F16 ? 2 : 3;
+    extern __shared__ uint8_t smem_raw[];
+    TcSmem<PARTS>& s = *reinterpret_cast<TcSmem<PARTS>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                       ~static_cast<uintptr_t>(1023));
+    constexpr uint32_t ID_S1 = tc::idesc_f16(!F16, CQ, CQ), ID_O2 = tc::idesc_f16(!F16, CQ, DV);
+    constexpr uint32_t ID_O = tc::idesc_f16(!F16, CQ, DV, true);
+    // the state's product reads both operands across their rows (A's bit is 15)
+    constexpr uint32_t ID_D = tc::idesc_f16(!F16, 128, DK, true) | (1u << 15);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c0 = blockIdx.x * DV, h = blockIdx.y, sq = blockIdx.z, hk = h / (a.H / a.Hk);
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&s.full[i], 1);
+            tc::mbar_init(&s.empty[i], 1 + 4);  // the chunk's last product, and the warps that read k
+            tc::mbar_init(&s.v_ok[i], 32);
+            tc::mbar_init(&s.tab_full[i], 32);
+            tc::mbar_init(&s.tab_empty[i], 8);
+        }
+        tc::mbar_init(&s.s1_full, 1);
+        tc::mbar_init(&s.p_full, 128);
+        tc::mbar_init(&s.o_full, 1);
+        tc::mbar_init(&s.o_free, 128);
+        tc::mbar_init(&s.s_ready, 128);
+        tc::mbar_init(&s.k_ready, 128);
+        tc::mbar_init(&s.k_max, 128);
+        tc::mbar_init(&s.d_done, 1);
+        tc::mbar_init(&s.drain, 1);
+        s.abort = 0;
+        s.dirty = 0;
+        tc::fence_mbar_init();
+        tc::prefetch_tmap(&tmQ);
+        tc::prefetch_tmap(&tmK);
+        tc::prefetch_tmap(&tmV);
+    }
+    // setup above touches no global memory; everything below may read the previous
+    // kernel's output
+    griddep_sync();
+    int start, len;
+    if (!ragged::sequence(a.cu, sq, a.total, &start, &len)) {
+        if (tid == 0) set_status(status, HYMBA_ERR_DEVICE_RANGE);
+        return;
+    }
+    const long long state_at = (((long long)sq * a.H + h) * a.dv + c0) * DK;
+    if (len == 0) {
+        if (a.state_out)
+            for (int i = tid; i < DV * DK; i += NT) a.state_out[state_at + i] = a.state_in ? a.state_in[state_at + i] : 0.f;
+        return;
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(&s.tmem_base, 512);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = s.tmem_base;
+    volatile int* abort = &s.abort;
+    const long long wlim = tc::wait_limit(status);
+    const int nc = (len + CQ - 1) / CQ;
+    int zero = 0;
+
+    if (warp == 0) {
+        // ---------------- TMA ----------------
+        if (lane == 0) {
+            int issued = 0;
+            for (int c = 0; c < nc; ++c) {
+                const int b = c & 1;
+                if (!tc::mbar_wait(&s.empty[b], ((c >> 1) & 1) ^ 1, abort, wlim)) { fail(abort, status, 0, c, 1); break; }
+                tc::mbar_arrive_expect_tx(&s.full[b], (2 + DV / 64) * TILE);
+                tc::tma_load_2d(s.q[b], &tmQ, &s.full[b], hk * DK, start + c * CQ);
+                tc::tma_load_2d(s.k[b], &tmK, &s.full[b], hk * DK, start + c * CQ);
+#pragma unroll
+                for (int p = 0; p < DV / 64; ++p)
+                    tc::tma_load_2d(s.v[b][p], &tmV, &s.full[b], h * a.dv + c0 + p * 64, start + c * CQ);
+                issued = c + 1;
+            }
+            // every copy issued has landed before the block exits
+            for (int c = max(0, issued - 2); c < issued; ++c) tc::mbar_wait(&s.full[c & 1], (c >> 1) & 1, &zero);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        if (tc::elect_one()) {
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t ph, int c, int id) {
+                if (ok && !tc::mbar_wait(bar, ph, abort, wlim)) {
+                    fail(abort, status, 1, c, id);
+                    ok = false;
+                }
+            };
+            for (int c = 0; ok && c < nc; ++c) {
+                const int b = c & 1;
+                const uint32_t ph2 = (c >> 1) & 1, ph = c & 1;
+                const uint32_t qa = tc::smem_u32(s.q[b]), ka = tc::smem_u32(s.k[b]), va = tc::smem_u32(s.v[b][0]);
+                wait(&s.full[b], ph2, c, 1);
+                if (c > 0) wait(&s.o_full, ph ^ 1, c, 2);  // S1 overwrites P
+                if (!ok) break;
+                tc::tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk)
+                    tc::mma_f16_ss(tmem + TM_S1, tc::sdesc_k_sw128(qa + kk * 32), tc::sdesc_k_sw128(ka + kk * 32), ID_S1, kk > 0);
+                tc::mma_commit(&s.s1_full);
+                // the state, once it is decayed and K' is there
+                wait(&s.s_ready, ph, c, 3);
+                wait(&s.v_ok[b], ph2, c, 4);
+                wait(&s.k_ready, ph, c, 5);
+                if (!ok) break;
+                tc::tc_fence_after();
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) {
+                    const uint32_t ks = tc::smem_u32(s.ks[p]);
+#pragma unroll
+                    for (int kk = 0; kk < CQ / 16; ++kk)
+                        tc::mma_f16_ss(tmem + TM_D, tc::sdesc_mn_sw128(va + kk * 2048, TILE),
+                                       tc::sdesc_mn_sw128(ks + kk * 2048, TILE), ID_D, 1);
+                }
+                tc::mma_commit(&s.d_done);
+                if (c > 0) wait(&s.o_free, ph ^ 1, c, 6);  // O and O2 of the chunk before are read
+                if (!ok) break;
+                tc::tc_fence_after();
+                const uint32_t sa = tc::smem_u32(s.s16[b]);
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk)
+                    tc::mma_f16_ss(tmem + TM_O2, tc::sdesc_k_sw128(qa + kk * 32), tc::sdesc_k_sw128(sa + kk * 32), ID_O2, kk > 0);
+                wait(&s.p_full, ph, c, 7);
+                if (!ok) break;
+                tc::tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < CQ / 16; ++kk)
+                    mma_f16_ts(tmem + TM_O, tmem + TM_S1 + kk * 8, tc::sdesc_mn_sw128(va + kk * 2048, TILE), ID_O, kk > 0);
+                tc::mma_commit(&s.o_full);
+                tc::mma_commit(&s.empty[b]);
+            }
+            // every MMA issued has completed before the block exits
+            tc::mma_commit(&s.drain);
+            tc::mbar_wait(&s.drain, 0, &zero);
+        }
+    } else if (warp == 2) {
+        // ---------------- decay tables ----------------
+        const float* g = a.g + start * a.ldg + h;
+        float x[4];
+        auto fetch = [&](int c) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = c * CQ + 4 * lane + i;
+                x[i] = t < len ? g[t * a.ldg] : 0.f;
+            }
+        };
+        fetch(0);
+        for (int c = 0; c < nc; ++c) {
+            const int b = c & 1;
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(&s.tab_empty[b], ((c >> 1) & 1) ^ 1, abort, wlim))) {
+                if (lane == 0) fail(abort, status, 0, c, 13);
+                break;
+            }
+            const float y[4] = {x[0], x[1], x[2], x[3]};
+            if (c + 1 < nc) fetch(c + 1);
+            make_tables(s.tab[b], y, len - c * CQ, a.log2_scale);
+            tc::mbar_arrive(&s.tab_full[b]);
+        }
+    } else if (warp == 3) {
+        // ---------------- V ----------------
+        for (int c = 0; c < nc; ++c) {
+            const int b = c & 1;
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(&s.full[b], (c >> 1) & 1, abort, wlim))) {
+                if (lane == 0) fail(abort, status, 0, c, 12);
+                break;
+            }
+            const int n = len - c * CQ;
+            uint8_t* vb = s.v[b][0];
+            // 0 x (not finite) is NaN; 16-byte piece x of panel p: row x / 8
+            typedef typename std::conditional<F16, __half2, __nv_bfloat162>::type P2;
+            uint32_t acc[4] = {0u, 0u, 0u, 0u};
+            const uint32_t nul = 0u;
+            for (int x = lane; x < CQ * 8 * (DV / 64); x += 32) {
+                uint4* at = reinterpret_cast<uint4*>(vb + x * 16);
+                if (((x >> 3) & (CQ - 1)) >= n) {
+                    *at = make_uint4(0, 0, 0, 0);
+                } else {
+                    const uint4 w = *at;
+                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const P2 r = __hfma2(*reinterpret_cast<const P2*>(&ww[i]), *reinterpret_cast<const P2*>(&nul),
+                                             *reinterpret_cast<const P2*>(&acc[i]));
+                        acc[i] = *reinterpret_cast<const uint32_t*>(&r);
+                    }
+                }
+            }
+            const bool odd = ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0;
+            if (__any_sync(0xffffffffu, odd) && lane == 0) *reinterpret_cast<volatile int*>(&s.dirty) = 1;
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(&s.v_ok[b]);
+        }
+    } else if (warp < 8) {
+        // ---------------- P and o: row i of the chunk, TMEM lane i ----------------
+        const int blk = warp & 3, i = blk * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(blk * 32) << 16;
+        const uint32_t s1 = tmem + lane_base + TM_S1, oc = tmem + lane_base + TM_O, o2c = tmem + lane_base + TM_O2;
+        T* orow = static_cast<T*>(a.o) + (start + (long long)i) * a.ldo + (long long)h * a.dv + c0;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t ph, int c, int id) {
+            if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(bar, ph, abort, wlim))) {
+                if (lane == 0) fail(abort, status, 2, c, id);
+                ok = false;
+            }
+        };
+        for (int c = 0; ok && c < nc; ++c, orow += CQ * a.ldo) {
+            const int b = c & 1;
+            const Tables& tab = s.tab[b];
+            wait(&s.tab_full[b], (c >> 1) & 1, c, 20);
+            wait(&s.s1_full, c & 1, c, 21);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const bool resets = tab.resets, grows = tab.grows;
+            const float ai = tab.a[i], ei = tab.e[i], Ai = fast_exp2(ai);
+            // the scores of block u, in place -> scale * decay * score, 0 above the diagonal
+            auto decayed = [&](int u, float (&x)[32]) {
+                if (u < blk) {
+                    if (!grows && !resets) {
+                        const float2 A2 = make_float2(Ai, Ai);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 B = *reinterpret_cast<const float4*>(&tab.B[blk - 1][32 * u + j]);
+                            const float2 y = __fmul2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), A2), make_float2(B.x, B.y));
+                            const float2 z = __fmul2_rn(__fmul2_rn(make_float2(x[j + 2], x[j + 3]), A2), make_float2(B.z, B.w));
+                            x[j] = y.x;
+                            x[j + 1] = y.y;
+                            x[j + 2] = z.x;
+                            x[j + 3] = z.y;
+                        }
+                    } else {
+                        const float base = ai + tab.between[blk][u];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[j] = fade(fast_exp2(base + tab.b[32 * u + j]), x[j]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 bj = *reinterpret_cast<const float4*>(&tab.b[32 * u + j]);
+                        const float d[4] = {fast_exp2(ai + bj.x), fast_exp2(ai + bj.y), fast_exp2(ai + bj.z), fast_exp2(ai + bj.w)};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float y = resets ? fade(d[e], x[j + e]) : d[e] * x[j + e];
+                            x[j + e] = j + e <= lane ? y : 0.f;
+                        }
+                    }
+                }
+            };
+            float f = 1.f;
+            if (F16) {
+                // the row's power of two, from its largest score (which bounds P unless a decay
+                // is above 1; then from P itself)
+                float mx = 0.f;
+#pragma unroll 1
+                for (int u = 0; u <= blk; ++u) {
+                    float x[32];
+                    ld32(s1 + 32 * u, x);
+                    tc::tmem_wait_ld();
+                    if (grows) decayed(u, x);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        // (behind the diagonal: keys the row does not see)
+                        const float x0 = u < blk || j <= lane ? fabsf(x[j]) : 0.f, x1 = u < blk || j + 1 <= lane ? fabsf(x[j + 1]) : 0.f;
+                        mx = fmax3(mx, x0, x1);
+                    }
+                }
+                f = to_middle(grows ? mx : mx * fast_exp2(a.log2_scale), -40, 40);
+            }
+            // P over the scores: block u goes to columns 16 u .. 16 u + 15, all read by then
+#pragma unroll 1
+            for (int u = 0; u < 4; u += 2) {
+                uint32_t pk[32];
+                float x[2][32];
+                if (u <= blk) ld32(s1 + 32 * u, x[0]);
+                if (u + 1 <= blk) ld32(s1 + 32 * (u + 1), x[1]);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (u + e <= blk) {
+                        decayed(u + e, x[e]);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2)
+                            pk[16 * e + j / 2] =
+                                F16 ? pack2<T>(x[e][j] * f, x[e][j + 1] * f) : pack2<T>(x[e][j], x[e][j + 1]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) pk[16 * e + j] = 0u;
+                    }
+                }
+                tc::tmem_st32(s1 + 16 * u, pk);
+            }
+            tc::tmem_wait_st();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&s.p_full);
+            wait(&s.o_full, c & 1, c, 22);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const float back = F16 ? inverse(f) : 1.f;
+            const bool in = c * CQ + i < len;
+#pragma unroll
+            for (int u = 0; u < DV / 32; ++u) {
+                float y[32], z[32];
+                ld32(oc + 32 * u, y);
+                ld32(o2c + 32 * u, z);
+                tc::tmem_wait_ld();
+                if (u == DV / 32 - 1) {
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(&s.o_free);
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    if (F16) z[j] *= s.col[b][32 * u + j];
+                    const float w = resets ? fade(ei, z[j]) : ei * z[j];
+                    y[j] = F16 ? fmaf(y[j], back, w) : y[j] + w;
+                }
+                if (in)
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8)
+                        *reinterpret_cast<uint4*>(orow + 32 * u + j) =
+                            make_uint4(pack2<T>(y[j], y[j + 1]), pack2<T>(y[j + 2], y[j + 3]), pack2<T>(y[j + 4], y[j + 5]),
+                                       pack2<T>(y[j + 6], y[j + 7]));
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&s.tab_empty[b]);
+        }
+    } else {
+        // ---------------- the state: row (value) and chunk row r ----------------
+        const int quad = warp & 3, r = quad * 32 + lane;
+        const uint32_t dc = tmem + ((uint32_t)(quad * 32) << 16) + TM_D;
+        const bool mine = quad * 32 < DV;  // the warp's rows are values of this block
+        float power = 1.f;                 // the state in TMEM is S * power (fp16)
+        float st[2][32];
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t ph, int c, int id) {
+            if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(bar, ph, abort, wlim))) {
+                if (lane == 0) fail(abort, status, 2, c, id);
+                ok = false;
+            }
+        };
+#pragma unroll
+        for (int e = 0; e < DK; e += 4) {
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (mine && a.state_in) y = *reinterpret_cast<const float4*>(a.state_in + state_at + (long long)r * DK + e);
+            st[e >> 5][e & 31] = y.x;
+            st[e >> 5][(e & 31) + 1] = y.y;
+            st[e >> 5][(e & 31) + 2] = y.z;
+            st[e >> 5][(e & 31) + 3] = y.w;
+        }
+        for (int c = 0; ok && c < nc; ++c) {
+            const int b = c & 1;
+            const Tables& tab = s.tab[b];
+            wait(&s.tab_full[b], (c >> 1) & 1, c, 30);
+            wait(&s.full[b], (c >> 1) & 1, c, 31);
+            if (!ok) break;
+            // row r of k (its 16-byte pieces swizzled by the row)
+            uint4 kr[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kr[e] = *reinterpret_cast<const uint4*>(s.k[b] + r * 128 + ((e ^ (r & 7)) * 16));
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&s.empty[b]);
+            const float w = tab.w[r];
+            const float dec0 = tab.dec;
+            float fk = 1.f;
+            if (F16) {
+                // the chunk's power for K': from the largest |w k|
+                float m = 0.f;
+                const uint32_t* kw = reinterpret_cast<const uint32_t*>(kr);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float2 y = unpack2<T>(kw[e]);
+                    m = fmax3(m, fabsf(y.x), fabsf(y.y));
+                }
+                m = fade(w, m);
+#pragma unroll
+                for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                if (lane == 0) s.kmax[b][quad] = m;
+                tc::mbar_arrive(&s.k_max);
+                wait(&s.k_max, c & 1, c, 34);
+                if (!ok) break;
+                fk = to_middle(fmaxf(fmaxf(s.kmax[b][0], s.kmax[b][1]), fmaxf(s.kmax[b][2], s.kmax[b][3])), -15, 24);
+            }
+            if (c > 0) {
+                wait(&s.d_done, (c - 1) & 1, c, 32);
+                if (!ok) break;
+                tc::tc_fence_after();
+                if (mine) {
+                    ld32(dc, st[0]);
+                    ld32(dc + 32, st[1]);
+                    tc::tmem_wait_ld();
+                }
+            }
+            if (mine) {
+                float fs = 1.f;
+                if (F16) {
+                    float m = 0.f;
+#pragma unroll
+                    for (int e = 0; e < DK; e += 2) m = fmax3(m, fabsf(st[e >> 5][e & 31]), fabsf(st[e >> 5][(e & 31) + 1]));
+                    fs = to_middle(m, -100, 100);
+                    s.col[b][r] = inverse(fs) * inverse(power);
+                }
+                uint8_t* row = s.s16[b] + r * 128;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float* y = &st[e >> 2][8 * (e & 3)];
+                    *reinterpret_cast<uint4*>(row + ((e ^ (r & 7)) * 16)) =
+                        make_uint4(pack2<T>(y[0] * fs, y[1] * fs), pack2<T>(y[2] * fs, y[3] * fs),
+                                   pack2<T>(y[4] * fs, y[5] * fs), pack2<T>(y[6] * fs, y[7] * fs));
+                }
+                const float dec = F16 ? dec0 * (fk * inverse(power)) : dec0;
+                if (dec0 == 0.f) {
+#pragma unroll
+                    for (int e = 0; e < DK; ++e) st[e >> 5][e & 31] = 0.f;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < DK; ++e) st[e >> 5][e & 31] *= dec;
+                }
+                tc::tmem_st32(dc, *reinterpret_cast<uint32_t(*)[32]>(&st[0]));
+                tc::tmem_st32(dc + 32, *reinterpret_cast<uint32_t(*)[32]>(&st[1]));
+                tc::tmem_wait_st();
+            }
+            power = fk;
+            tc::fence_proxy_async_smem();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&s.s_ready);
+            // K' (its buffers are free: the state's product of the chunk before is done)
+            const float2 w2 = make_float2(w * fk, w * fk);
+            const bool drop = w == 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t kw[4] = {kr[e].x, kr[e].y, kr[e].z, kr[e].w};
+                uint32_t part[PARTS][4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    float2 y = drop ? make_float2(0.f, 0.f) : __fmul2_rn(unpack2<T>(kw[x]), w2);
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p) {
+                        part[p][x] = pack2<T>(y.x, y.y);
+                        if (p + 1 < PARTS) {
+                            const float2 z = unpack2<T>(part[p][x]);
+                            y.x -= z.x;
+                            y.y -= z.y;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p)
+                    *reinterpret_cast<uint4*>(s.ks[p] + r * 128 + ((e ^ (r & 7)) * 16)) =
+                        make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
+            }
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(&s.k_ready);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&s.tab_empty[b]);
+        }
+        wait(&s.d_done, (nc - 1) & 1, nc, 33);
+        if (ok && mine && a.state_out && !*reinterpret_cast<volatile int*>(&s.dirty)) {
+            tc::tc_fence_after();
+            ld32(dc, st[0]);
+            ld32(dc + 32, st[1]);
+            tc::tmem_wait_ld();
+            const float back = F16 ? inverse(power) : 1.f;
+            float* to = a.state_out + state_at + (long long)r * DK;
+#pragma unroll
+            for (int e = 0; e < DK; e += 4)
+                *reinterpret_cast<float4*>(to + e) =
+                    make_float4(st[e >> 5][e & 31] * back, st[e >> 5][(e & 31) + 1] * back, st[e >> 5][(e & 31) + 2] * back,
+                                st[e >> 5][(e & 31) + 3] * back);
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, 512);
+    }
+    if (s.dirty && !s.abort && tid >= 128 && tid < 128 + DV) recurrence<T>(a, sq, h, start, len, c0 + tid - 128);
+}
+
+template <typename T, int DV>
+int launch_dv(const Ctx& ctx, const LinAttn& x) {
+    constexpr bool BF16 = std::is_same<T, bf16>::value;
+    CUtensorMap tq, tk, tv;
+    if (!tc::make_tmap_2d(&tq, x.q, BF16, x.total, (uint64_t)x.Hk * DK, x.ldq, CQ) ||
+        !tc::make_tmap_2d(&tk, x.k, BF16, x.total, (uint64_t)x.Hk * DK, x.ldk, CQ) ||
+        !tc::make_tmap_2d(&tv, x.v, BF16, x.total, (uint64_t)x.H * x.dv, x.ldv, CQ))
+        return HYMBA_ERR_UNSUPPORTED;
+    auto kern = linattn_tc_kernel<T, DV>;
+    const size_t smem = sizeof(TcSmem<BF16 ? 3 : 2>) + 1024;
+    static std::atomic<unsigned long long> smem_set{0};
+    if (!smem_opt_in_once(smem_set, kern, smem, ctx)) return HYMBA_ERR_CUDA;
+    // sequences on the grid's slowest dimension, in runs it can hold
+    for (int s0 = 0; s0 < x.n_seqs; s0 += 65535) {
+        const int n = x.n_seqs - s0 < 65535 ? x.n_seqs - s0 : 65535;
+        const long long st0 = (long long)s0 * x.H * x.dv * DK;
+        Args a;
+        a.q = x.q; a.k = x.k; a.v = x.v; a.o = x.o;
+        a.ldq = x.ldq; a.ldk = x.ldk; a.ldv = x.ldv; a.ldo = x.ldo; a.ldg = x.ldg;
+        a.g = x.g;
+        a.state_in = x.state_in ? x.state_in + st0 : nullptr;
+        a.state_out = x.state_out ? x.state_out + st0 : nullptr;
+        a.cu = x.cu + s0;
+        a.total = x.total; a.Hk = x.Hk; a.H = x.H; a.dv = x.dv;
+        a.log2_scale = log2f(x.scale);
+        HYMBA_LAUNCH(ctx, "linattn_chunk", kern, dim3(x.dv / DV, x.H, n), NT, smem, tq, tk, tv, a, ctx.status);
+    }
+    return HYMBA_OK;
+}
+
+}  // namespace
+
+bool linattn_tc_applies(const LinAttn& a) { return a.dk == DK && a.total > 0; }
+
+template <typename T>
+int launch_linattn_tc(const Ctx& ctx, const LinAttn& a) {
+    return a.dv % 128 == 0 ? launch_dv<T, 128>(ctx, a) : launch_dv<T, 64>(ctx, a);
+}
+template int launch_linattn_tc<f16>(const Ctx&, const LinAttn&);
+template int launch_linattn_tc<bf16>(const Ctx&, const LinAttn&);
+
+}  // namespace hymba

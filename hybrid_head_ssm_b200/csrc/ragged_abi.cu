@@ -177,6 +177,7 @@ int hymba_linattn_prefill(const hymba_linattn_shape* shape, const void* q, int64
     a.n_seqs = n_seqs;
     a.total = total_rows;
     if (shape->dtype == HYMBA_F32) return launch_linattn_recurrent<float>(ctx, a);
+    if (linattn_tc_applies(a)) return shape->dtype == HYMBA_F16 ? launch_linattn_tc<f16>(ctx, a) : launch_linattn_tc<bf16>(ctx, a);
     if (shape->dtype == HYMBA_F16) return launch_linattn_chunk<f16>(ctx, a);
     return launch_linattn_chunk<bf16>(ctx, a);
 }
