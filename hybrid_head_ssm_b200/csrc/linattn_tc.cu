@@ -6,21 +6,23 @@
 //     o_i = scale (sum_{j<=i} exp(cs_i - cs_j) (q_i . k_j) v_j  +  exp(cs_i) S q_i)
 //     S  <- exp(cs_128) S + sum_j exp(cs_128 - cs_j) v_j k_j^T
 //
-// One CTA per (64 or 128 value columns, head, sequence) walks the chunks. 12 warps:
+// One CTA per (64 or 128 value columns, head, sequence) walks the chunks. 16 warps:
 //   warp 0      TMA of q, k, v, two chunks deep;
 //   warp 1      TMEM, and one thread that issues the four products of a chunk:
 //               S1 = q k^T (128 x 128 x 64), D += V^T K' (the state, values x keys, both
 //               operands read across their rows), O2 = q S^T, O = P V (P from TMEM over S1);
 //   warp 2      the decay tables of the next chunk from 64-bit sums;
 //   warp 3      V: rows behind the sequence become zero, values that are not finite are noted;
-//   warps 4-7   one thread per row i: P = mask * decay * scale * S1 as 16-bit pairs into TMEM,
-//               then o_i = O + exp(cs_i) scale O2 to global memory;
-//   warps 8-11  one thread per state row (value) and chunk row: the state from TMEM, its
-//               16-bit copy for O2 to shared memory, the decayed state back; then K' = exp(cs_128 -
-//               cs_j) k_j as 16-bit parts in shared memory.
-// The chains of the two warpgroups overlap: while P and o of a chunk are formed, the state
-// group prepares the products of the same chunk, and S1 of the next follows the last read of P.
-//
+//   warps 4-7   one thread per row i: P = mask * decay * scale * S1 as 16-bit pairs into TMEM;
+//   warps 8-11  one thread per row j: K' = exp(cs_128 - cs_j) k_j as 16-bit parts in shared memory;
+//   warps 12-15 one thread per state row (value): the state from TMEM, its 16-bit copy for O2 to
+//               shared memory, the decayed state back; then, one thread per row i of the chunk
+//               before, o_i = O + exp(cs_i) scale O2, through that chunk's q and k tiles (no
+//               longer needed) to global memory by TMA, the rows of the last chunk one by one.
+// The longest chain is S1 -> P -> P V of one chunk after the other (S1 overwrites P); the state
+// and K' of a chunk are formed under it. Loops over a row are kept rolled: the warps run
+// different code, and what does not fit the instruction caches together is fetched again every
+// chunk (unrolled, 3.8 of every 5 stalls were waits for instructions and a chunk took twice as long).
 // Numbers: a decay between rows of different 32-row blocks is A_i B_j, both distances from
 // the start of i's block and so at most 1 each (a chunk with a positive log decay forms
 // 2^(a_i + b_j) instead), within a block 2^(a_i + b_j). K' enters as three parts (bf16) or two
@@ -41,7 +43,8 @@ namespace {
 
 constexpr int CQ = 128;  // rows per chunk
 constexpr int DK = 64;
-constexpr int NT = 384;
+constexpr int NT = 512;
+constexpr int NTAB = 4;  // chunks whose tables are kept
 constexpr int TILE = CQ * 128;  // bytes of 128 rows x 64 16-bit columns
 // TMEM columns: S1 / P, O, O2, the state
 constexpr uint32_t TM_S1 = 0, TM_O = 128, TM_O2 = 256, TM_D = 384;
@@ -66,11 +69,12 @@ struct TcSmem {
     alignas(1024) uint8_t v[2][2][TILE];
     alignas(1024) uint8_t ks[PARTS][TILE];  // K' parts, rows j
     alignas(1024) uint8_t s16[2][TILE];     // the state's copy, rows = values
-    Tables tab[2];
+    Tables tab[NTAB];
     float col[2][CQ];  // fp16: 1 / power of two of the copy's rows
+    float ps[2][CQ];   // fp16: the power of two of P's rows
     float kmax[2][4];
-    uint64_t full[2], empty[2], v_ok[2], tab_full[2], tab_empty[2];
-    uint64_t s1_full, p_full, o_full, o_free, s_ready, k_ready, k_max, d_done, drain;
+    uint64_t full[2], v_ok[2], tab_full[NTAB], tab_empty[NTAB];
+    uint64_t s1_full, p_full, o_full, o_free, o_staged, s_ready, k_ready, k_max, d_done, drain;
     uint32_t tmem_base;
     int abort, dirty;
 };
@@ -102,6 +106,11 @@ __device__ __forceinline__ float to_middle(float x, int low, int high) {
 __device__ __forceinline__ float inverse(float p) { return __int_as_float(0x7f000000 - __float_as_int(p)); }
 // a decay of 0 drops what it multiplies, also what is not finite
 __device__ __forceinline__ float fade(float d, float x) { return d == 0.f ? 0.f : d * x; }
+
+// the power of two of a chunk's K' from its four warps' largest values
+__device__ __forceinline__ float k_power(const float* m) {
+    return to_middle(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), -15, 24);
+}
 
 template <typename T>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -215,7 +224,8 @@ __device__ __forceinline__ void ld32(uint32_t addr, float (&x)[32]) {
 template <typename T, int DV>
 __global__ void __launch_bounds__(NT, 1)
 linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                  const __grid_constant__ CUtensorMap tmV, const Args a, int* status) {
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const Args a,
+                  int* status) {
     constexpr bool F16 = std::is_same<T, f16>::value;
     constexpr int PARTS = F16 ? 2 : 3;
     extern __shared__ uint8_t smem_raw[];
@@ -231,11 +241,13 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&s.full[i], 1);
-            tc::mbar_init(&s.empty[i], 1 + 4);  // the chunk's last product, and the warps that read k
             tc::mbar_init(&s.v_ok[i], 32);
-            tc::mbar_init(&s.tab_full[i], 32);
-            tc::mbar_init(&s.tab_empty[i], 8);
         }
+        for (int i = 0; i < NTAB; ++i) {
+            tc::mbar_init(&s.tab_full[i], 32);
+            tc::mbar_init(&s.tab_empty[i], 12);
+        }
+        tc::mbar_init(&s.o_staged, 128);
         tc::mbar_init(&s.s1_full, 1);
         tc::mbar_init(&s.p_full, 128);
         tc::mbar_init(&s.o_full, 1);
@@ -251,6 +263,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         tc::prefetch_tmap(&tmQ);
         tc::prefetch_tmap(&tmK);
         tc::prefetch_tmap(&tmV);
+        tc::prefetch_tmap(&tmO);
     }
     // setup above touches no global memory; everything below may read the previous
     // kernel's output
@@ -280,12 +293,11 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     int zero = 0;
 
     if (warp == 0) {
-        // ---------------- TMA ----------------
+        // ---------------- TMA: q, k, v in, o out of the tiles of q and k ----------------
         if (lane == 0) {
             int issued = 0;
-            for (int c = 0; c < nc; ++c) {
+            auto load = [&](int c) {
                 const int b = c & 1;
-                if (!tc::mbar_wait(&s.empty[b], ((c >> 1) & 1) ^ 1, abort, wlim)) { fail(abort, status, 0, c, 1); break; }
                 tc::mbar_arrive_expect_tx(&s.full[b], (2 + DV / 64) * TILE);
                 tc::tma_load_2d(s.q[b], &tmQ, &s.full[b], hk * DK, start + c * CQ);
                 tc::tma_load_2d(s.k[b], &tmK, &s.full[b], hk * DK, start + c * CQ);
@@ -293,9 +305,24 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 for (int p = 0; p < DV / 64; ++p)
                     tc::tma_load_2d(s.v[b][p], &tmV, &s.full[b], h * a.dv + c0 + p * 64, start + c * CQ);
                 issued = c + 1;
+            };
+            load(0);
+            if (nc > 1) load(1);
+            // (the last chunk's rows leave one by one)
+            for (int c = 0; c + 1 < nc; ++c) {
+                const int b = c & 1;
+                if (!tc::mbar_wait(&s.o_staged, c & 1, abort, wlim)) { fail(abort, status, 0, c, 1); break; }
+                tc::tma_store_2d(&tmO, s.q[b], h * a.dv + c0, start + c * CQ);
+                if (DV == 128) tc::tma_store_2d(&tmO, s.k[b], h * a.dv + c0 + 64, start + c * CQ);
+                tc::tma_store_commit();
+                if (c + 2 < nc) {
+                    tc::tma_store_wait_read();
+                    load(c + 2);
+                }
             }
             // every copy issued has landed before the block exits
             for (int c = max(0, issued - 2); c < issued; ++c) tc::mbar_wait(&s.full[c & 1], (c >> 1) & 1, &zero);
+            tc::tma_store_wait();
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
@@ -348,7 +375,6 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 for (int kk = 0; kk < CQ / 16; ++kk)
                     mma_f16_ts(tmem + TM_O, tmem + TM_S1 + kk * 8, tc::sdesc_mn_sw128(va + kk * 2048, TILE), ID_O, kk > 0);
                 tc::mma_commit(&s.o_full);
-                tc::mma_commit(&s.empty[b]);
             }
             // every MMA issued has completed before the block exits
             tc::mma_commit(&s.drain);
@@ -367,15 +393,14 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         };
         fetch(0);
         for (int c = 0; c < nc; ++c) {
-            const int b = c & 1;
-            if (!__all_sync(0xffffffffu, tc::mbar_wait(&s.tab_empty[b], ((c >> 1) & 1) ^ 1, abort, wlim))) {
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(&s.tab_empty[c % NTAB], ((c / NTAB) & 1) ^ 1, abort, wlim))) {
                 if (lane == 0) fail(abort, status, 0, c, 13);
                 break;
             }
             const float y[4] = {x[0], x[1], x[2], x[3]};
             if (c + 1 < nc) fetch(c + 1);
-            make_tables(s.tab[b], y, len - c * CQ, a.log2_scale);
-            tc::mbar_arrive(&s.tab_full[b]);
+            make_tables(s.tab[c % NTAB], y, len - c * CQ, a.log2_scale);
+            tc::mbar_arrive(&s.tab_full[c % NTAB]);
         }
     } else if (warp == 3) {
         // ---------------- V ----------------
@@ -386,18 +411,23 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 break;
             }
             const int n = len - c * CQ;
-            uint8_t* vb = s.v[b][0];
             // 0 x (not finite) is NaN; 16-byte piece x of panel p: row x / 8
             typedef typename std::conditional<F16, __half2, __nv_bfloat162>::type P2;
+            uint4* vb = reinterpret_cast<uint4*>(s.v[b][0]);
+            constexpr int PIECES = CQ * 8 * (DV / 64);
+            if (n < CQ)
+                for (int x = lane; x < PIECES; x += 32)
+                    if (((x >> 3) & (CQ - 1)) >= n) vb[x] = make_uint4(0, 0, 0, 0);
             uint32_t acc[4] = {0u, 0u, 0u, 0u};
             const uint32_t nul = 0u;
-            for (int x = lane; x < CQ * 8 * (DV / 64); x += 32) {
-                uint4* at = reinterpret_cast<uint4*>(vb + x * 16);
-                if (((x >> 3) & (CQ - 1)) >= n) {
-                    *at = make_uint4(0, 0, 0, 0);
-                } else {
-                    const uint4 w = *at;
-                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll 1
+            for (int x = lane; x < PIECES; x += 32 * 8) {
+                uint4 w[8];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) w[y] = vb[x + 32 * y];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    const uint32_t ww[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const P2 r = __hfma2(*reinterpret_cast<const P2*>(&ww[i]), *reinterpret_cast<const P2*>(&nul),
@@ -412,11 +442,10 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             tc::mbar_arrive(&s.v_ok[b]);
         }
     } else if (warp < 8) {
-        // ---------------- P and o: row i of the chunk, TMEM lane i ----------------
+        // ---------------- P: row i of the chunk, TMEM lane i ----------------
         const int blk = warp & 3, i = blk * 32 + lane;
         const uint32_t lane_base = (uint32_t)(blk * 32) << 16;
-        const uint32_t s1 = tmem + lane_base + TM_S1, oc = tmem + lane_base + TM_O, o2c = tmem + lane_base + TM_O2;
-        T* orow = static_cast<T*>(a.o) + (start + (long long)i) * a.ldo + (long long)h * a.dv + c0;
+        const uint32_t s1 = tmem + lane_base + TM_S1;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t ph, int c, int id) {
             if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(bar, ph, abort, wlim))) {
@@ -424,15 +453,15 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 ok = false;
             }
         };
-        for (int c = 0; ok && c < nc; ++c, orow += CQ * a.ldo) {
+        for (int c = 0; ok && c < nc; ++c) {
             const int b = c & 1;
-            const Tables& tab = s.tab[b];
-            wait(&s.tab_full[b], (c >> 1) & 1, c, 20);
+            const Tables& tab = s.tab[c % NTAB];
+            wait(&s.tab_full[c % NTAB], (c / NTAB) & 1, c, 20);
             wait(&s.s1_full, c & 1, c, 21);
             if (!ok) break;
             tc::tc_fence_after();
             const bool resets = tab.resets, grows = tab.grows;
-            const float ai = tab.a[i], ei = tab.e[i], Ai = fast_exp2(ai);
+            const float ai = tab.a[i], Ai = fast_exp2(ai);
             // the scores of block u, in place -> scale * decay * score, 0 above the diagonal
             auto decayed = [&](int u, float (&x)[32]) {
                 if (u < blk) {
@@ -485,71 +514,42 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     }
                 }
                 f = to_middle(grows ? mx : mx * fast_exp2(a.log2_scale), -40, 40);
+                s.ps[b][i] = f;
             }
             // P over the scores: block u goes to columns 16 u .. 16 u + 15, all read by then
-#pragma unroll 1
-            for (int u = 0; u < 4; u += 2) {
-                uint32_t pk[32];
+            {
                 float x[2][32];
-                if (u <= blk) ld32(s1 + 32 * u, x[0]);
-                if (u + 1 <= blk) ld32(s1 + 32 * (u + 1), x[1]);
-                tc::tmem_wait_ld();
+                ld32(s1, x[0]);
+#pragma unroll 1
+                for (int u0 = 0; u0 < 4; u0 += 2)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (u + e <= blk) {
-                        decayed(u + e, x[e]);
+                    for (int e = 0; e < 2; ++e) {
+                        // (the load after this one flies under this block's arithmetic)
+                        const int u = u0 + e;
+                        uint32_t pk[16];
+                        if (u <= blk) {
+                            tc::tmem_wait_ld();
+                            if (u < blk) ld32(s1 + 32 * (u + 1), x[e ^ 1]);
+                            decayed(u, x[e]);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2)
-                            pk[16 * e + j / 2] =
-                                F16 ? pack2<T>(x[e][j] * f, x[e][j + 1] * f) : pack2<T>(x[e][j], x[e][j + 1]);
-                    } else {
+                            for (int j = 0; j < 32; j += 2)
+                                pk[j / 2] = F16 ? pack2<T>(x[e][j] * f, x[e][j + 1] * f) : pack2<T>(x[e][j], x[e][j + 1]);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) pk[16 * e + j] = 0u;
+                            for (int j = 0; j < 16; ++j) pk[j] = 0u;
+                        }
+                        tc::tmem_st16(s1 + 16 * u, pk);
                     }
-                }
-                tc::tmem_st32(s1 + 16 * u, pk);
             }
             tc::tmem_wait_st();
             tc::tc_fence_before();
             tc::mbar_arrive(&s.p_full);
-            wait(&s.o_full, c & 1, c, 22);
-            if (!ok) break;
-            tc::tc_fence_after();
-            const float back = F16 ? inverse(f) : 1.f;
-            const bool in = c * CQ + i < len;
-#pragma unroll
-            for (int u = 0; u < DV / 32; ++u) {
-                float y[32], z[32];
-                ld32(oc + 32 * u, y);
-                ld32(o2c + 32 * u, z);
-                tc::tmem_wait_ld();
-                if (u == DV / 32 - 1) {
-                    tc::tc_fence_before();
-                    tc::mbar_arrive(&s.o_free);
-                }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    if (F16) z[j] *= s.col[b][32 * u + j];
-                    const float w = resets ? fade(ei, z[j]) : ei * z[j];
-                    y[j] = F16 ? fmaf(y[j], back, w) : y[j] + w;
-                }
-                if (in)
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8)
-                        *reinterpret_cast<uint4*>(orow + 32 * u + j) =
-                            make_uint4(pack2<T>(y[j], y[j + 1]), pack2<T>(y[j + 2], y[j + 3]), pack2<T>(y[j + 4], y[j + 5]),
-                                       pack2<T>(y[j + 6], y[j + 7]));
-            }
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&s.tab_empty[b]);
+            if (lane == 0) tc::mbar_arrive(&s.tab_empty[c % NTAB]);
         }
-    } else {
-        // ---------------- the state: row (value) and chunk row r ----------------
+    } else if (warp < 12) {
+        // ---------------- K': row r of the chunk ----------------
         const int quad = warp & 3, r = quad * 32 + lane;
-        const uint32_t dc = tmem + ((uint32_t)(quad * 32) << 16) + TM_D;
-        const bool mine = quad * 32 < DV;  // the warp's rows are values of this block
-        float power = 1.f;                 // the state in TMEM is S * power (fp16)
-        float st[2][32];
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t ph, int c, int id) {
             if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(bar, ph, abort, wlim))) {
@@ -557,38 +557,27 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 ok = false;
             }
         };
-#pragma unroll
-        for (int e = 0; e < DK; e += 4) {
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (mine && a.state_in) y = *reinterpret_cast<const float4*>(a.state_in + state_at + (long long)r * DK + e);
-            st[e >> 5][e & 31] = y.x;
-            st[e >> 5][(e & 31) + 1] = y.y;
-            st[e >> 5][(e & 31) + 2] = y.z;
-            st[e >> 5][(e & 31) + 3] = y.w;
-        }
         for (int c = 0; ok && c < nc; ++c) {
             const int b = c & 1;
-            const Tables& tab = s.tab[b];
-            wait(&s.tab_full[b], (c >> 1) & 1, c, 30);
+            const Tables& tab = s.tab[c % NTAB];
+            wait(&s.tab_full[c % NTAB], (c / NTAB) & 1, c, 30);
             wait(&s.full[b], (c >> 1) & 1, c, 31);
             if (!ok) break;
-            // row r of k (its 16-byte pieces swizzled by the row)
-            uint4 kr[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) kr[e] = *reinterpret_cast<const uint4*>(s.k[b] + r * 128 + ((e ^ (r & 7)) * 16));
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&s.empty[b]);
+            const uint8_t* krow = s.k[b] + r * 128;  // its 16-byte pieces are swizzled by the row
             const float w = tab.w[r];
-            const float dec0 = tab.dec;
             float fk = 1.f;
             if (F16) {
                 // the chunk's power for K': from the largest |w k|
                 float m = 0.f;
-                const uint32_t* kw = reinterpret_cast<const uint32_t*>(kr);
+#pragma unroll 2
+                for (int e = 0; e < 8; ++e) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(krow + (e ^ (r & 7)) * 16);
+                    const uint32_t kw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float2 y = unpack2<T>(kw[e]);
-                    m = fmax3(m, fabsf(y.x), fabsf(y.y));
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 y = unpack2<T>(kw[i]);
+                        m = fmax3(m, fabsf(y.x), fabsf(y.y));
+                    }
                 }
                 m = fade(w, m);
 #pragma unroll
@@ -597,57 +586,17 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 tc::mbar_arrive(&s.k_max);
                 wait(&s.k_max, c & 1, c, 34);
                 if (!ok) break;
-                fk = to_middle(fmaxf(fmaxf(s.kmax[b][0], s.kmax[b][1]), fmaxf(s.kmax[b][2], s.kmax[b][3])), -15, 24);
+                fk = k_power(s.kmax[b]);
             }
-            if (c > 0) {
-                wait(&s.d_done, (c - 1) & 1, c, 32);
-                if (!ok) break;
-                tc::tc_fence_after();
-                if (mine) {
-                    ld32(dc, st[0]);
-                    ld32(dc + 32, st[1]);
-                    tc::tmem_wait_ld();
-                }
-            }
-            if (mine) {
-                float fs = 1.f;
-                if (F16) {
-                    float m = 0.f;
-#pragma unroll
-                    for (int e = 0; e < DK; e += 2) m = fmax3(m, fabsf(st[e >> 5][e & 31]), fabsf(st[e >> 5][(e & 31) + 1]));
-                    fs = to_middle(m, -100, 100);
-                    s.col[b][r] = inverse(fs) * inverse(power);
-                }
-                uint8_t* row = s.s16[b] + r * 128;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float* y = &st[e >> 2][8 * (e & 3)];
-                    *reinterpret_cast<uint4*>(row + ((e ^ (r & 7)) * 16)) =
-                        make_uint4(pack2<T>(y[0] * fs, y[1] * fs), pack2<T>(y[2] * fs, y[3] * fs),
-                                   pack2<T>(y[4] * fs, y[5] * fs), pack2<T>(y[6] * fs, y[7] * fs));
-                }
-                const float dec = F16 ? dec0 * (fk * inverse(power)) : dec0;
-                if (dec0 == 0.f) {
-#pragma unroll
-                    for (int e = 0; e < DK; ++e) st[e >> 5][e & 31] = 0.f;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < DK; ++e) st[e >> 5][e & 31] *= dec;
-                }
-                tc::tmem_st32(dc, *reinterpret_cast<uint32_t(*)[32]>(&st[0]));
-                tc::tmem_st32(dc + 32, *reinterpret_cast<uint32_t(*)[32]>(&st[1]));
-                tc::tmem_wait_st();
-            }
-            power = fk;
-            tc::fence_proxy_async_smem();
-            tc::tc_fence_before();
-            tc::mbar_arrive(&s.s_ready);
-            // K' (its buffers are free: the state's product of the chunk before is done)
+            if (c > 0) wait(&s.d_done, (c - 1) & 1, c, 32);  // the buffers are free
+            if (!ok) break;
             const float2 w2 = make_float2(w * fk, w * fk);
             const bool drop = w == 0.f;
-#pragma unroll
+#pragma unroll 4
             for (int e = 0; e < 8; ++e) {
-                const uint32_t kw[4] = {kr[e].x, kr[e].y, kr[e].z, kr[e].w};
+                const int at = (e ^ (r & 7)) * 16;
+                const uint4 x4 = *reinterpret_cast<const uint4*>(krow + at);
+                const uint32_t kw[4] = {x4.x, x4.y, x4.z, x4.w};
                 uint32_t part[PARTS][4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -657,34 +606,173 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         part[p][x] = pack2<T>(y.x, y.y);
                         if (p + 1 < PARTS) {
                             const float2 z = unpack2<T>(part[p][x]);
-                            y.x -= z.x;
-                            y.y -= z.y;
+                            y = __fadd2_rn(y, make_float2(-z.x, -z.y));
                         }
                     }
                 }
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p)
-                    *reinterpret_cast<uint4*>(s.ks[p] + r * 128 + ((e ^ (r & 7)) * 16)) =
+                    *reinterpret_cast<uint4*>(s.ks[p] + r * 128 + at) =
                         make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
             }
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(&s.k_ready);
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&s.tab_empty[b]);
+            if (lane == 0) tc::mbar_arrive(&s.tab_empty[c % NTAB]);
+        }
+    } else {
+        // ---------------- the state (row r a value), then o (row r of the chunk) ----------------
+        const int quad = warp & 3, r = quad * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        const uint32_t dc = tmem + lane_base + TM_D, oc = tmem + lane_base + TM_O, o2c = tmem + lane_base + TM_O2;
+        const bool mine = quad * 32 < DV;  // the warp's rows are values of this block
+        float power = 1.f;                 // the state in TMEM is S * power (fp16)
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t ph, int c, int id) {
+            if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(bar, ph, abort, wlim))) {
+                if (lane == 0) fail(abort, status, 2, c, id);
+                ok = false;
+            }
+        };
+        if (mine) {
+#pragma unroll 1
+            for (int u = 0; u < DK; u += 32) {
+                float y[32];
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (a.state_in) z = *reinterpret_cast<const float4*>(a.state_in + state_at + (long long)r * DK + u + e);
+                    y[e] = z.x;
+                    y[e + 1] = z.y;
+                    y[e + 2] = z.z;
+                    y[e + 3] = z.w;
+                }
+                tc::tmem_st32(dc + u, *reinterpret_cast<uint32_t(*)[32]>(&y));
+            }
+            tc::tmem_wait_st();
+        }
+        for (int c = 0; ok && c <= nc; ++c) {
+            if (c < nc) {
+                // the state before chunk c
+                const int b = c & 1;
+                wait(&s.tab_full[c % NTAB], (c / NTAB) & 1, c, 35);
+                if (F16) wait(&s.k_max, c & 1, c, 36);
+                if (c > 0) wait(&s.d_done, (c - 1) & 1, c, 37);
+                if (!ok) break;
+                tc::tc_fence_after();
+                if (mine) {
+                    const float dec0 = s.tab[c % NTAB].dec;
+                    float fs = 1.f, dec = dec0;
+                    if (F16) {
+                        float m = 0.f;
+#pragma unroll 1
+                        for (int u = 0; u < DK; u += 32) {
+                            float y[32];
+                            ld32(dc + u, y);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) m = fmax3(m, fabsf(y[e]), fabsf(y[e + 1]));
+                        }
+                        fs = to_middle(m, -100, 100);
+                        s.col[b][r] = inverse(fs) * inverse(power);
+                        const float fk = k_power(s.kmax[b]);
+                        dec = dec0 * (fk * inverse(power));
+                        power = fk;
+                    }
+                    uint8_t* row = s.s16[b] + r * 128;
+#pragma unroll 1
+                    for (int u = 0; u < DK; u += 32) {
+                        float y[32];
+                        ld32(dc + u, y);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4*>(row + ((((u + e) >> 3) ^ (r & 7)) * 16)) =
+                                make_uint4(pack2<T>(y[e] * fs, y[e + 1] * fs), pack2<T>(y[e + 2] * fs, y[e + 3] * fs),
+                                           pack2<T>(y[e + 4] * fs, y[e + 5] * fs), pack2<T>(y[e + 6] * fs, y[e + 7] * fs));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) y[e] = dec0 == 0.f ? 0.f : y[e] * dec;
+                        tc::tmem_st32(dc + u, *reinterpret_cast<uint32_t(*)[32]>(&y));
+                    }
+                    tc::tmem_wait_st();
+                }
+                tc::fence_proxy_async_smem();
+                tc::tc_fence_before();
+                tc::mbar_arrive(&s.s_ready);
+            }
+            if (c > 0) {
+                // o of chunk c - 1
+                const int p = c - 1, b = p & 1;
+                const Tables& tab = s.tab[p % NTAB];
+                wait(&s.o_full, p & 1, c, 38);
+                if (!ok) break;
+                tc::tc_fence_after();
+                const bool resets = tab.resets;
+                const float ei = tab.e[r], back = F16 ? inverse(s.ps[b][r]) : 1.f;
+                // the last product of the chunk is done: its q and k tiles take o's columns
+                uint32_t y[2][16], z[2][16];
+                tc::tmem_ld16(oc, y[0]);
+                tc::tmem_ld16(o2c, z[0]);
+#pragma unroll 1
+                for (int u0 = 0; u0 < DV / 16; u0 += 2)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int u = u0 + e;
+                        tc::tmem_wait_ld();
+                        if (u + 1 < DV / 16) {
+                            tc::tmem_ld16(oc + 16 * (u + 1), y[e ^ 1]);
+                            tc::tmem_ld16(o2c + 16 * (u + 1), z[e ^ 1]);
+                        }
+                        uint8_t* row = (u < 4 ? s.q[b] : s.k[b]) + r * 128;
+                        uint32_t w8[8];
+#pragma unroll
+                        for (int x = 0; x < 16; x += 2) {
+                            float v[2];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                float t = __uint_as_float(z[e][x + i]);
+                                if (F16) t *= s.col[b][16 * u + x + i];
+                                t = resets ? fade(ei, t) : ei * t;
+                                v[i] = F16 ? fmaf(__uint_as_float(y[e][x + i]), back, t) : __uint_as_float(y[e][x + i]) + t;
+                            }
+                            w8[x / 2] = pack2<T>(v[0], v[1]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            *reinterpret_cast<uint4*>(row + (((2 * (u & 3) + i) ^ (r & 7)) * 16)) =
+                                make_uint4(w8[4 * i], w8[4 * i + 1], w8[4 * i + 2], w8[4 * i + 3]);
+                    }
+                tc::tc_fence_before();
+                tc::mbar_arrive(&s.o_free);
+                if (c < nc) {
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&s.o_staged);
+                } else if (p * CQ + r < len) {
+                    T* orow = static_cast<T*>(a.o) + (start + (long long)p * CQ + r) * a.ldo + (long long)h * a.dv + c0;
+#pragma unroll 1
+                    for (int e = 0; e < DV / 8; ++e)
+                        *reinterpret_cast<uint4*>(orow + 8 * e) = *reinterpret_cast<const uint4*>(
+                            (e < 8 ? s.q[b] : s.k[b]) + r * 128 + (((e & 7) ^ (r & 7)) * 16));
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&s.tab_empty[p % NTAB]);
+            }
         }
         wait(&s.d_done, (nc - 1) & 1, nc, 33);
         if (ok && mine && a.state_out && !*reinterpret_cast<volatile int*>(&s.dirty)) {
             tc::tc_fence_after();
-            ld32(dc, st[0]);
-            ld32(dc + 32, st[1]);
-            tc::tmem_wait_ld();
             const float back = F16 ? inverse(power) : 1.f;
             float* to = a.state_out + state_at + (long long)r * DK;
+#pragma unroll 1
+            for (int u = 0; u < DK; u += 32) {
+                float y[32];
+                ld32(dc + u, y);
+                tc::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < DK; e += 4)
-                *reinterpret_cast<float4*>(to + e) =
-                    make_float4(st[e >> 5][e & 31] * back, st[e >> 5][(e & 31) + 1] * back, st[e >> 5][(e & 31) + 2] * back,
-                                st[e >> 5][(e & 31) + 3] * back);
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4*>(to + u + e) =
+                        make_float4(y[e] * back, y[e + 1] * back, y[e + 2] * back, y[e + 3] * back);
+            }
         }
     }
     tc::tc_fence_before();
@@ -699,10 +787,11 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 template <typename T, int DV>
 int launch_dv(const Ctx& ctx, const LinAttn& x) {
     constexpr bool BF16 = std::is_same<T, bf16>::value;
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tk, tv, to;
     if (!tc::make_tmap_2d(&tq, x.q, BF16, x.total, (uint64_t)x.Hk * DK, x.ldq, CQ) ||
         !tc::make_tmap_2d(&tk, x.k, BF16, x.total, (uint64_t)x.Hk * DK, x.ldk, CQ) ||
-        !tc::make_tmap_2d(&tv, x.v, BF16, x.total, (uint64_t)x.H * x.dv, x.ldv, CQ))
+        !tc::make_tmap_2d(&tv, x.v, BF16, x.total, (uint64_t)x.H * x.dv, x.ldv, CQ) ||
+        !tc::make_tmap_2d(&to, x.o, BF16, x.total, (uint64_t)x.H * x.dv, x.ldo, CQ))
         return HYMBA_ERR_UNSUPPORTED;
     auto kern = linattn_tc_kernel<T, DV>;
     const size_t smem = sizeof(TcSmem<BF16 ? 3 : 2>) + 1024;
@@ -721,7 +810,7 @@ int launch_dv(const Ctx& ctx, const LinAttn& x) {
         a.cu = x.cu + s0;
         a.total = x.total; a.Hk = x.Hk; a.H = x.H; a.dv = x.dv;
         a.log2_scale = log2f(x.scale);
-        HYMBA_LAUNCH(ctx, "linattn_chunk", kern, dim3(x.dv / DV, x.H, n), NT, smem, tq, tk, tv, a, ctx.status);
+        HYMBA_LAUNCH(ctx, "linattn_chunk", kern, dim3(x.dv / DV, x.H, n), NT, smem, tq, tk, tv, to, a, ctx.status);
     }
     return HYMBA_OK;
 }
