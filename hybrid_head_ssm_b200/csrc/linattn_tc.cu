@@ -14,18 +14,18 @@
 //   warp 2      the decay tables of the next chunk from 64-bit sums;
 //   warp 3      V: rows behind the sequence become zero, values that are not finite are noted;
 //   warps 4-7   one thread per row i: P = mask * decay * scale * S1 as 16-bit pairs into TMEM;
-//   warps 8-11  one thread per row j: K' = exp(cs_128 - cs_j) k_j as 16-bit parts in shared memory;
-//   warps 12-15 one thread per state row (value): the state from TMEM, its 16-bit copy for O2 to
-//               shared memory, the decayed state back; then, one thread per row i of the chunk
-//               before, o_i = O + exp(cs_i) scale O2, through that chunk's q and k tiles (no
-//               longer needed) to global memory by TMA, the rows of the last chunk one by one.
+//   warps 8-11  one thread per state row (value): the state from TMEM, its 16-bit copy for O2 to
+//               shared memory, the decayed state back; then, one thread per row j, K' =
+//               exp(cs_128 - cs_j) k_j as 16-bit parts in shared memory;
+//   warps 12-15 one thread per row i: o_i = O + exp(cs_i) scale O2 to global memory.
 // The longest chain is S1 -> P -> P V of one chunk after the other (S1 overwrites P); the state
 // and K' of a chunk are formed under it. Loops over a row are kept rolled: the warps run
 // different code, and what does not fit the instruction caches together is fetched again every
 // chunk (unrolled, 3.8 of every 5 stalls were waits for instructions and a chunk took twice as long).
 // Numbers: a decay between rows of different 32-row blocks is A_i B_j, both distances from
 // the start of i's block and so at most 1 each (a chunk with a positive log decay forms
-// 2^(a_i + b_j) instead), within a block 2^(a_i + b_j). K' enters as three parts (bf16) or two
+// 2^(a_i + b_j) instead), within a block 2^(a_i + b_j); either way right to fp32 after any other
+// row (one that forgets everything included). K' enters as three parts (bf16) or two
 // (fp16), at least 22 bits of every term of the fp32 state; P and the state's copy are rounded
 // to the rows' type, like any MMA operand. fp16 has little range: P's rows, the copy's rows and
 // K' are brought to the middle of it by powers of two that the fp32 values give back (the
@@ -44,7 +44,7 @@ namespace {
 constexpr int CQ = 128;  // rows per chunk
 constexpr int DK = 64;
 constexpr int NT = 512;
-constexpr int NTAB = 4;  // chunks whose tables are kept
+constexpr int NTAB = 2;  // chunks whose tables are kept
 constexpr int TILE = CQ * 128;  // bytes of 128 rows x 64 16-bit columns
 // TMEM columns: S1 / P, O, O2, the state
 constexpr uint32_t TM_S1 = 0, TM_O = 128, TM_O2 = 256, TM_D = 384;
@@ -69,15 +69,18 @@ struct TcSmem {
     alignas(1024) uint8_t v[2][2][TILE];
     alignas(1024) uint8_t ks[PARTS][TILE];  // K' parts, rows j
     alignas(1024) uint8_t s16[2][TILE];     // the state's copy, rows = values
+    alignas(128) uint8_t mid[4][32 * 64];   // o of each warp on its way out, 32 columns at a time
     Tables tab[NTAB];
     float col[2][CQ];  // fp16: 1 / power of two of the copy's rows
     float ps[2][CQ];   // fp16: the power of two of P's rows
     float kmax[2][4];
     uint64_t full[2], v_ok[2], tab_full[NTAB], tab_empty[NTAB];
-    uint64_t s1_full, p_full, o_full, o_free, o_staged, s_ready, k_ready, k_max, d_done, drain;
+    uint64_t s1_full, p_full, o_full, o_free, s_ready, k_ready, k_max, d_done, drain;
     uint32_t tmem_base;
     int abort, dirty;
 };
+
+static_assert(sizeof(TcSmem<3>) + 1024 <= 227 * 1024, "more than a block's shared memory");
 
 struct Args {
     const void *q, *k, *v;
@@ -107,84 +110,84 @@ __device__ __forceinline__ float inverse(float p) { return __int_as_float(0x7f00
 // a decay of 0 drops what it multiplies, also what is not finite
 __device__ __forceinline__ float fade(float d, float x) { return d == 0.f ? 0.f : d * x; }
 
-// the power of two of a chunk's K' from its four warps' largest values
-__device__ __forceinline__ float k_power(const float* m) {
-    return to_middle(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), -15, 24);
-}
-
 template <typename T>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
     const T* x = reinterpret_cast<const T*>(&w);
     return make_float2(to_f(x[0]), to_f(x[1]));
 }
 
-// the tables of one chunk; lane l holds the log decays of rows 4 l .. 4 l + 3; n rows are real
-__device__ __forceinline__ void make_tables(Tables& t, const float (&g)[4], int n, float lsc) {
-    constexpr double LOG2E = 1.4426950408889634;
-    const int lane = threadIdx.x & 31, blk = lane >> 3;
-    double d[4], x[4];
-    float down = 0.f;
-    bool up = false;
+// A lane's part of the tables of one chunk, from the log decays of rows 4 l .. 4 l + 3; n rows
+// are real.
+struct LaneTables {
+    float a[4], b[4], e[4], w[4], B[3][4], between, dec;
+    int resets, grows;
+    __device__ __forceinline__ void make(const float (&g)[4], int n, float lsc) {
+        constexpr double LOG2E = 1.4426950408889634;
+        const int lane = threadIdx.x & 31, blk = lane >> 3;
+        double d[4];
+        float down = 0.f;
+        bool up = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        d[i] = (double)g[i] * LOG2E;
-        // a decay below 2^-160 is 0 in fp32; the limit keeps -infinity out of the sums
-        if (d[i] < -160.0) d[i] = -160.0;
-        down += fminf((float)d[i], 0.f);
-        up |= !(d[i] <= 0.0);
-    }
-    double sum = (d[0] + d[1]) + (d[2] + d[3]);
-    const double own = sum;
+        for (int i = 0; i < 4; ++i) {
+            d[i] = (double)g[i] * LOG2E;
+            // a decay below 2^-160 is 0 in fp32; the limit keeps -infinity out of the sums
+            if (d[i] < -160.0) d[i] = -160.0;
+            down += fminf(g[i], 0.f);
+            up |= !(g[i] <= 0.f);
+        }
+        const double own = (d[0] + d[1]) + (d[2] + d[3]);
+        double sum = own;
 #pragma unroll
-    for (int w = 1; w < 32; w <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, sum, w);
-        if (lane >= w) sum += y;
-    }
-    const double last = __shfl_sync(0xffffffffu, sum, 31);
-    double c[4] = {0.0, __shfl_sync(0xffffffffu, sum, 7), __shfl_sync(0xffffffffu, sum, 15),
-                   __shfl_sync(0xffffffffu, sum, 23)};
-    const double from = blk == 0 ? c[0] : blk == 1 ? c[1] : blk == 2 ? c[2] : c[3];
-    double before = __shfl_up_sync(0xffffffffu, sum, 1);
-    if (lane == 0) before = 0.0;
-    (void)own;
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        const double last = __shfl_sync(0xffffffffu, sum, 31);
+        const double c1 = __shfl_sync(0xffffffffu, sum, 7), c2 = __shfl_sync(0xffffffffu, sum, 15),
+                     c3 = __shfl_sync(0xffffffffu, sum, 23);
+        const double from = blk == 0 ? 0.0 : blk == 1 ? c1 : blk == 2 ? c2 : c3;
+        double before = __shfl_up_sync(0xffffffffu, sum, 1);
+        if (lane == 0) before = 0.0;
+        double x = before;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        before += d[i];
-        x[i] = before;
-    }
-    float va[4], vb[4], ve[4], vw[4];
+        for (int i = 0; i < 4; ++i) {
+            x += d[i];
+            a[i] = (float)(x - from) + lsc;
+            b[i] = (float)(from - x);
+            e[i] = fast_exp2((float)x + lsc);
+            w[i] = 4 * lane + i < n ? fast_exp2((float)(last - x)) : 0.f;
+            B[0][i] = fast_exp2((float)(c1 - x));
+            B[1][i] = fast_exp2((float)(c2 - x));
+            B[2][i] = fast_exp2((float)(c3 - x));
+        }
+        const int r = (lane >> 2) & 3, u = lane & 3;
+        const double cr = r == 0 ? 0.0 : r == 1 ? c1 : r == 2 ? c2 : c3;
+        const double cu = u == 0 ? 0.0 : u == 1 ? c1 : u == 2 ? c2 : c3;
+        between = (float)(cr - cu);
+        grows = __any_sync(0xffffffffu, up);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        va[i] = (float)(x[i] - from) + lsc;
-        vb[i] = (float)(from - x[i]);
-        ve[i] = fast_exp2((float)x[i] + lsc);
-        vw[i] = 4 * lane + i < n ? fast_exp2((float)(last - x[i])) : 0.f;
+        for (int o = 16; o; o >>= 1) down += __shfl_xor_sync(0xffffffffu, down, o);
+        dec = fast_exp2((float)last);
+        resets = !(down * 1.4426950f + fminf(lsc, 0.f) > -120.f);
     }
-    *reinterpret_cast<float4*>(&t.a[4 * lane]) = make_float4(va[0], va[1], va[2], va[3]);
-    *reinterpret_cast<float4*>(&t.b[4 * lane]) = make_float4(vb[0], vb[1], vb[2], vb[3]);
-    *reinterpret_cast<float4*>(&t.e[4 * lane]) = make_float4(ve[0], ve[1], ve[2], ve[3]);
-    *reinterpret_cast<float4*>(&t.w[4 * lane]) = make_float4(vw[0], vw[1], vw[2], vw[3]);
+    __device__ __forceinline__ void store(Tables& t) const {
+        const int lane = threadIdx.x & 31, blk = lane >> 3;
+        auto put = [](float* to, const float (&x)[4]) { *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]); };
+        put(&t.a[4 * lane], a);
+        put(&t.b[4 * lane], b);
+        put(&t.e[4 * lane], e);
+        put(&t.w[4 * lane], w);
 #pragma unroll
-    for (int b = 1; b < 4; ++b)
-        if (blk < b)
-            *reinterpret_cast<float4*>(&t.B[b - 1][4 * lane]) =
-                make_float4(fast_exp2((float)(c[b] - x[0])), fast_exp2((float)(c[b] - x[1])),
-                            fast_exp2((float)(c[b] - x[2])), fast_exp2((float)(c[b] - x[3])));
-    if (lane < 16) {
-        const int r = lane >> 2, u = lane & 3;
-        const double cr = r == 0 ? c[0] : r == 1 ? c[1] : r == 2 ? c[2] : c[3];
-        const double cu = u == 0 ? c[0] : u == 1 ? c[1] : u == 2 ? c[2] : c[3];
-        t.between[r][u] = (float)(cr - cu);
+        for (int i = 0; i < 3; ++i)
+            if (blk <= i) put(&t.B[i][4 * lane], B[i]);
+        if (lane < 16) t.between[lane >> 2][lane & 3] = between;
+        if (lane == 0) {
+            t.dec = dec;
+            t.resets = resets;
+            t.grows = grows;
+        }
     }
-    up = __any_sync(0xffffffffu, up);
-#pragma unroll
-    for (int w = 16; w; w >>= 1) down += __shfl_xor_sync(0xffffffffu, down, w);
-    if (lane == 0) {
-        t.dec = fast_exp2((float)last);
-        t.resets = !(down + fminf(lsc, 0.f) > -120.f);
-        t.grows = up;
-    }
-}
+};
 
 // One value column of a sequence by the recurrence.
 template <typename T>
@@ -216,6 +219,40 @@ __device__ __noinline__ void recurrence(const Args& a, int s, int h, int start, 
         for (int e = 0; e < DK; ++e) a.state_out[at + e] = S[e];
 }
 
+// Row r of K' = w k as parts of T; w = 0 drops the row. The 16-byte pieces are swizzled by the row.
+template <typename T, int PARTS>
+__device__ __forceinline__ void scaled_keys(uint8_t (*ks)[TILE], const uint8_t* krow, int r, float w) {
+    const float2 w2 = make_float2(w, w);
+    const bool drop = w == 0.f;
+#pragma unroll 2
+    for (int e = 0; e < 8; ++e) {
+        const int at = (e ^ (r & 7)) * 16;
+        const uint4 x4 = *reinterpret_cast<const uint4*>(krow + at);
+        const uint32_t kw[4] = {x4.x, x4.y, x4.z, x4.w};
+        uint32_t part[PARTS][4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            float2 y = drop ? make_float2(0.f, 0.f) : __fmul2_rn(unpack2<T>(kw[x]), w2);
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+                part[p][x] = pack2<T>(y.x, y.y);
+                if (p + 1 < PARTS) {
+                    const float2 z = unpack2<T>(part[p][x]);
+                    y = __fadd2_rn(y, make_float2(-z.x, -z.y));
+                }
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p)
+            *reinterpret_cast<uint4*>(ks[p] + r * 128 + at) = make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
+    }
+}
+
+// the power of two of a chunk's K' from its four warps' largest values
+__device__ __forceinline__ float k_power(const float* m) {
+    return to_middle(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), -15, 24);
+}
+
 // 32 lanes x 32 columns of fp32, read
 __device__ __forceinline__ void ld32(uint32_t addr, float (&x)[32]) {
     tc::tmem_ld32(addr, *reinterpret_cast<uint32_t(*)[32]>(&x));
@@ -224,8 +261,7 @@ __device__ __forceinline__ void ld32(uint32_t addr, float (&x)[32]) {
 template <typename T, int DV>
 __global__ void __launch_bounds__(NT, 1)
 linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const Args a,
-                  int* status) {
+                  const __grid_constant__ CUtensorMap tmV, const Args a, int* status) {
     constexpr bool F16 = std::is_same<T, f16>::value;
     constexpr int PARTS = F16 ? 2 : 3;
     extern __shared__ uint8_t smem_raw[];
@@ -247,7 +283,6 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             tc::mbar_init(&s.tab_full[i], 32);
             tc::mbar_init(&s.tab_empty[i], 12);
         }
-        tc::mbar_init(&s.o_staged, 128);
         tc::mbar_init(&s.s1_full, 1);
         tc::mbar_init(&s.p_full, 128);
         tc::mbar_init(&s.o_full, 1);
@@ -263,7 +298,6 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         tc::prefetch_tmap(&tmQ);
         tc::prefetch_tmap(&tmK);
         tc::prefetch_tmap(&tmV);
-        tc::prefetch_tmap(&tmO);
     }
     // setup above touches no global memory; everything below may read the previous
     // kernel's output
@@ -293,11 +327,13 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     int zero = 0;
 
     if (warp == 0) {
-        // ---------------- TMA: q, k, v in, o out of the tiles of q and k ----------------
+        // ---------------- TMA ----------------
         if (lane == 0) {
             int issued = 0;
-            auto load = [&](int c) {
+            for (int c = 0; c < nc; ++c) {
                 const int b = c & 1;
+                // the stage's chunk is done with its last product, which follows every read of it
+                if (c > 1 && !tc::mbar_wait(&s.o_full, c & 1, abort, wlim)) { fail(abort, status, 0, c, 1); break; }
                 tc::mbar_arrive_expect_tx(&s.full[b], (2 + DV / 64) * TILE);
                 tc::tma_load_2d(s.q[b], &tmQ, &s.full[b], hk * DK, start + c * CQ);
                 tc::tma_load_2d(s.k[b], &tmK, &s.full[b], hk * DK, start + c * CQ);
@@ -305,24 +341,9 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 for (int p = 0; p < DV / 64; ++p)
                     tc::tma_load_2d(s.v[b][p], &tmV, &s.full[b], h * a.dv + c0 + p * 64, start + c * CQ);
                 issued = c + 1;
-            };
-            load(0);
-            if (nc > 1) load(1);
-            // (the last chunk's rows leave one by one)
-            for (int c = 0; c + 1 < nc; ++c) {
-                const int b = c & 1;
-                if (!tc::mbar_wait(&s.o_staged, c & 1, abort, wlim)) { fail(abort, status, 0, c, 1); break; }
-                tc::tma_store_2d(&tmO, s.q[b], h * a.dv + c0, start + c * CQ);
-                if (DV == 128) tc::tma_store_2d(&tmO, s.k[b], h * a.dv + c0 + 64, start + c * CQ);
-                tc::tma_store_commit();
-                if (c + 2 < nc) {
-                    tc::tma_store_wait_read();
-                    load(c + 2);
-                }
             }
             // every copy issued has landed before the block exits
             for (int c = max(0, issued - 2); c < issued; ++c) tc::mbar_wait(&s.full[c & 1], (c >> 1) & 1, &zero);
-            tc::tma_store_wait();
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
@@ -393,13 +414,14 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         };
         fetch(0);
         for (int c = 0; c < nc; ++c) {
+            LaneTables t;
+            t.make(x, len - c * CQ, a.log2_scale);
+            if (c + 1 < nc) fetch(c + 1);
             if (!__all_sync(0xffffffffu, tc::mbar_wait(&s.tab_empty[c % NTAB], ((c / NTAB) & 1) ^ 1, abort, wlim))) {
                 if (lane == 0) fail(abort, status, 0, c, 13);
                 break;
             }
-            const float y[4] = {x[0], x[1], x[2], x[3]};
-            if (c + 1 < nc) fetch(c + 1);
-            make_tables(s.tab[c % NTAB], y, len - c * CQ, a.log2_scale);
+            t.store(s.tab[c % NTAB]);
             tc::mbar_arrive(&s.tab_full[c % NTAB]);
         }
     } else if (warp == 3) {
@@ -460,37 +482,35 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             wait(&s.s1_full, c & 1, c, 21);
             if (!ok) break;
             tc::tc_fence_after();
-            const bool resets = tab.resets, grows = tab.grows;
+            const bool grows = tab.grows, plain = !grows && !tab.resets;
             const float ai = tab.a[i], Ai = fast_exp2(ai);
-            // the scores of block u, in place -> scale * decay * score, 0 above the diagonal
+            // columns 32 u .. 32 u + 31 of the scores, in place -> scale * decay * score, 0 above the
+            // diagonal
             auto decayed = [&](int u, float (&x)[32]) {
-                if (u < blk) {
-                    if (!grows && !resets) {
-                        const float2 A2 = make_float2(Ai, Ai);
+                if (u < blk && plain) {
+                    const float2 A2 = make_float2(Ai, Ai);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 B = *reinterpret_cast<const float4*>(&tab.B[blk - 1][32 * u + j]);
-                            const float2 y = __fmul2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), A2), make_float2(B.x, B.y));
-                            const float2 z = __fmul2_rn(__fmul2_rn(make_float2(x[j + 2], x[j + 3]), A2), make_float2(B.z, B.w));
-                            x[j] = y.x;
-                            x[j + 1] = y.y;
-                            x[j + 2] = z.x;
-                            x[j + 3] = z.y;
-                        }
-                    } else {
-                        const float base = ai + tab.between[blk][u];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = fade(fast_exp2(base + tab.b[32 * u + j]), x[j]);
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 B = *reinterpret_cast<const float4*>(&tab.B[blk - 1][32 * u + j]);
+                        const float2 y = __fmul2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), A2), make_float2(B.x, B.y));
+                        const float2 z = __fmul2_rn(__fmul2_rn(make_float2(x[j + 2], x[j + 3]), A2), make_float2(B.z, B.w));
+                        x[j] = y.x;
+                        x[j + 1] = y.y;
+                        x[j + 2] = z.x;
+                        x[j + 3] = z.y;
                     }
                 } else {
+                    const float base = ai + tab.between[blk][u];
+                    const int last = u < blk ? 31 : lane;
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
                         const float4 bj = *reinterpret_cast<const float4*>(&tab.b[32 * u + j]);
-                        const float d[4] = {fast_exp2(ai + bj.x), fast_exp2(ai + bj.y), fast_exp2(ai + bj.z), fast_exp2(ai + bj.w)};
+                        const float d[4] = {bj.x, bj.y, bj.z, bj.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float y = resets ? fade(d[e], x[j + e]) : d[e] * x[j + e];
-                            x[j + e] = j + e <= lane ? y : 0.f;
+                            // (a decay of 0 drops what it multiplies, also what is not finite)
+                            const float w = fast_exp2(base + d[e]);
+                            x[j + e] = j + e <= last && w != 0.f ? w * x[j + e] : 0.f;
                         }
                     }
                 }
@@ -506,40 +526,31 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     ld32(s1 + 32 * u, x);
                     tc::tmem_wait_ld();
                     if (grows) decayed(u, x);
+                    const int last = u < blk ? 31 : lane;  // (behind the diagonal: keys the row does not see)
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        // (behind the diagonal: keys the row does not see)
-                        const float x0 = u < blk || j <= lane ? fabsf(x[j]) : 0.f, x1 = u < blk || j + 1 <= lane ? fabsf(x[j + 1]) : 0.f;
-                        mx = fmax3(mx, x0, x1);
-                    }
+                    for (int j = 0; j < 32; j += 2)
+                        mx = fmax3(mx, j <= last ? fabsf(x[j]) : 0.f, j + 1 <= last ? fabsf(x[j + 1]) : 0.f);
                 }
                 f = to_middle(grows ? mx : mx * fast_exp2(a.log2_scale), -40, 40);
                 s.ps[b][i] = f;
             }
             // P over the scores: block u goes to columns 16 u .. 16 u + 15, all read by then
-            {
-                float x[2][32];
-                ld32(s1, x[0]);
 #pragma unroll 1
-                for (int u0 = 0; u0 < 4; u0 += 2)
+            for (int u = 0; u < 4; ++u) {
+                uint32_t pk[16];
+                if (u <= blk) {
+                    float x[32];
+                    ld32(s1 + 32 * u, x);
+                    tc::tmem_wait_ld();
+                    decayed(u, x);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        // (the load after this one flies under this block's arithmetic)
-                        const int u = u0 + e;
-                        uint32_t pk[16];
-                        if (u <= blk) {
-                            tc::tmem_wait_ld();
-                            if (u < blk) ld32(s1 + 32 * (u + 1), x[e ^ 1]);
-                            decayed(u, x[e]);
+                    for (int j = 0; j < 32; j += 2)
+                        pk[j / 2] = F16 ? pack2<T>(x[j] * f, x[j + 1] * f) : pack2<T>(x[j], x[j + 1]);
+                } else {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 2)
-                                pk[j / 2] = F16 ? pack2<T>(x[e][j] * f, x[e][j + 1] * f) : pack2<T>(x[e][j], x[e][j + 1]);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) pk[j] = 0u;
-                        }
-                        tc::tmem_st16(s1 + 16 * u, pk);
-                    }
+                    for (int j = 0; j < 16; ++j) pk[j] = 0u;
+                }
+                tc::tmem_st16(s1 + 16 * u, pk);
             }
             tc::tmem_wait_st();
             tc::tc_fence_before();
@@ -548,83 +559,9 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             if (lane == 0) tc::mbar_arrive(&s.tab_empty[c % NTAB]);
         }
     } else if (warp < 12) {
-        // ---------------- K': row r of the chunk ----------------
+        // ---------------- the state (row r a value), then K' (row r of the chunk) ----------------
         const int quad = warp & 3, r = quad * 32 + lane;
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t ph, int c, int id) {
-            if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(bar, ph, abort, wlim))) {
-                if (lane == 0) fail(abort, status, 2, c, id);
-                ok = false;
-            }
-        };
-        for (int c = 0; ok && c < nc; ++c) {
-            const int b = c & 1;
-            const Tables& tab = s.tab[c % NTAB];
-            wait(&s.tab_full[c % NTAB], (c / NTAB) & 1, c, 30);
-            wait(&s.full[b], (c >> 1) & 1, c, 31);
-            if (!ok) break;
-            const uint8_t* krow = s.k[b] + r * 128;  // its 16-byte pieces are swizzled by the row
-            const float w = tab.w[r];
-            float fk = 1.f;
-            if (F16) {
-                // the chunk's power for K': from the largest |w k|
-                float m = 0.f;
-#pragma unroll 2
-                for (int e = 0; e < 8; ++e) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(krow + (e ^ (r & 7)) * 16);
-                    const uint32_t kw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 y = unpack2<T>(kw[i]);
-                        m = fmax3(m, fabsf(y.x), fabsf(y.y));
-                    }
-                }
-                m = fade(w, m);
-#pragma unroll
-                for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-                if (lane == 0) s.kmax[b][quad] = m;
-                tc::mbar_arrive(&s.k_max);
-                wait(&s.k_max, c & 1, c, 34);
-                if (!ok) break;
-                fk = k_power(s.kmax[b]);
-            }
-            if (c > 0) wait(&s.d_done, (c - 1) & 1, c, 32);  // the buffers are free
-            if (!ok) break;
-            const float2 w2 = make_float2(w * fk, w * fk);
-            const bool drop = w == 0.f;
-#pragma unroll 4
-            for (int e = 0; e < 8; ++e) {
-                const int at = (e ^ (r & 7)) * 16;
-                const uint4 x4 = *reinterpret_cast<const uint4*>(krow + at);
-                const uint32_t kw[4] = {x4.x, x4.y, x4.z, x4.w};
-                uint32_t part[PARTS][4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    float2 y = drop ? make_float2(0.f, 0.f) : __fmul2_rn(unpack2<T>(kw[x]), w2);
-#pragma unroll
-                    for (int p = 0; p < PARTS; ++p) {
-                        part[p][x] = pack2<T>(y.x, y.y);
-                        if (p + 1 < PARTS) {
-                            const float2 z = unpack2<T>(part[p][x]);
-                            y = __fadd2_rn(y, make_float2(-z.x, -z.y));
-                        }
-                    }
-                }
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p)
-                    *reinterpret_cast<uint4*>(s.ks[p] + r * 128 + at) =
-                        make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
-            }
-            tc::fence_proxy_async_smem();
-            tc::mbar_arrive(&s.k_ready);
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&s.tab_empty[c % NTAB]);
-        }
-    } else {
-        // ---------------- the state (row r a value), then o (row r of the chunk) ----------------
-        const int quad = warp & 3, r = quad * 32 + lane;
-        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-        const uint32_t dc = tmem + lane_base + TM_D, oc = tmem + lane_base + TM_O, o2c = tmem + lane_base + TM_O2;
+        const uint32_t dc = tmem + ((uint32_t)(quad * 32) << 16) + TM_D;
         const bool mine = quad * 32 < DV;  // the warp's rows are values of this block
         float power = 1.f;                 // the state in TMEM is S * power (fp16)
         bool ok = true;
@@ -651,112 +588,82 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             }
             tc::tmem_wait_st();
         }
-        for (int c = 0; ok && c <= nc; ++c) {
-            if (c < nc) {
-                // the state before chunk c
-                const int b = c & 1;
-                wait(&s.tab_full[c % NTAB], (c / NTAB) & 1, c, 35);
-                if (F16) wait(&s.k_max, c & 1, c, 36);
-                if (c > 0) wait(&s.d_done, (c - 1) & 1, c, 37);
-                if (!ok) break;
-                tc::tc_fence_after();
-                if (mine) {
-                    const float dec0 = s.tab[c % NTAB].dec;
-                    float fs = 1.f, dec = dec0;
-                    if (F16) {
-                        float m = 0.f;
-#pragma unroll 1
-                        for (int u = 0; u < DK; u += 32) {
-                            float y[32];
-                            ld32(dc + u, y);
-                            tc::tmem_wait_ld();
+        for (int c = 0; ok && c < nc; ++c) {
+            const int b = c & 1;
+            const Tables& tab = s.tab[c % NTAB];
+            wait(&s.tab_full[c % NTAB], (c / NTAB) & 1, c, 30);
+            wait(&s.full[b], (c >> 1) & 1, c, 31);
+            if (!ok) break;
+            const uint8_t* krow = s.k[b] + r * 128;  // its 16-byte pieces are swizzled by the row
+            const float w = tab.w[r], dec0 = tab.dec;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&s.tab_empty[c % NTAB]);
+            float fk = 1.f;
+            if (F16) {
+                // the chunk's power for K': from the largest |w k|
+                float m = 0.f;
+#pragma unroll 2
+                for (int e = 0; e < 8; ++e) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(krow + (e ^ (r & 7)) * 16);
+                    const uint32_t kw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) m = fmax3(m, fabsf(y[e]), fabsf(y[e + 1]));
-                        }
-                        fs = to_middle(m, -100, 100);
-                        s.col[b][r] = inverse(fs) * inverse(power);
-                        const float fk = k_power(s.kmax[b]);
-                        dec = dec0 * (fk * inverse(power));
-                        power = fk;
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 y = unpack2<T>(kw[i]);
+                        m = fmax3(m, fabsf(y.x), fabsf(y.y));
                     }
-                    uint8_t* row = s.s16[b] + r * 128;
+                }
+                m = fade(w, m);
+#pragma unroll
+                for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                if (lane == 0) s.kmax[b][quad] = m;
+                tc::mbar_arrive(&s.k_max);
+                wait(&s.k_max, c & 1, c, 34);
+                if (!ok) break;
+                fk = k_power(s.kmax[b]);
+            }
+            if (c > 0) wait(&s.d_done, (c - 1) & 1, c, 32);  // the state is whole, K' buffers are free
+            if (!ok) break;
+            tc::tc_fence_after();
+            if (mine) {
+                float fs = 1.f, dec = dec0;
+                if (F16) {
+                    float m = 0.f;
 #pragma unroll 1
                     for (int u = 0; u < DK; u += 32) {
                         float y[32];
                         ld32(dc + u, y);
                         tc::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4*>(row + ((((u + e) >> 3) ^ (r & 7)) * 16)) =
-                                make_uint4(pack2<T>(y[e] * fs, y[e + 1] * fs), pack2<T>(y[e + 2] * fs, y[e + 3] * fs),
-                                           pack2<T>(y[e + 4] * fs, y[e + 5] * fs), pack2<T>(y[e + 6] * fs, y[e + 7] * fs));
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) y[e] = dec0 == 0.f ? 0.f : y[e] * dec;
-                        tc::tmem_st32(dc + u, *reinterpret_cast<uint32_t(*)[32]>(&y));
+                        for (int e = 0; e < 32; e += 2) m = fmax3(m, fabsf(y[e]), fabsf(y[e + 1]));
                     }
-                    tc::tmem_wait_st();
+                    fs = to_middle(m, -100, 100);
+                    s.col[b][r] = inverse(fs) * inverse(power);
+                    dec = dec0 * (fk * inverse(power));
                 }
-                tc::fence_proxy_async_smem();
-                tc::tc_fence_before();
-                tc::mbar_arrive(&s.s_ready);
-            }
-            if (c > 0) {
-                // o of chunk c - 1
-                const int p = c - 1, b = p & 1;
-                const Tables& tab = s.tab[p % NTAB];
-                wait(&s.o_full, p & 1, c, 38);
-                if (!ok) break;
-                tc::tc_fence_after();
-                const bool resets = tab.resets;
-                const float ei = tab.e[r], back = F16 ? inverse(s.ps[b][r]) : 1.f;
-                // the last product of the chunk is done: its q and k tiles take o's columns
-                uint32_t y[2][16], z[2][16];
-                tc::tmem_ld16(oc, y[0]);
-                tc::tmem_ld16(o2c, z[0]);
+                uint8_t* row = s.s16[b] + r * 128;
 #pragma unroll 1
-                for (int u0 = 0; u0 < DV / 16; u0 += 2)
+                for (int u = 0; u < DK; u += 32) {
+                    float y[32];
+                    ld32(dc + u, y);
+                    tc::tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int u = u0 + e;
-                        tc::tmem_wait_ld();
-                        if (u + 1 < DV / 16) {
-                            tc::tmem_ld16(oc + 16 * (u + 1), y[e ^ 1]);
-                            tc::tmem_ld16(o2c + 16 * (u + 1), z[e ^ 1]);
-                        }
-                        uint8_t* row = (u < 4 ? s.q[b] : s.k[b]) + r * 128;
-                        uint32_t w8[8];
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4*>(row + ((((u + e) >> 3) ^ (r & 7)) * 16)) =
+                            make_uint4(pack2<T>(y[e] * fs, y[e + 1] * fs), pack2<T>(y[e + 2] * fs, y[e + 3] * fs),
+                                       pack2<T>(y[e + 4] * fs, y[e + 5] * fs), pack2<T>(y[e + 6] * fs, y[e + 7] * fs));
 #pragma unroll
-                        for (int x = 0; x < 16; x += 2) {
-                            float v[2];
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                float t = __uint_as_float(z[e][x + i]);
-                                if (F16) t *= s.col[b][16 * u + x + i];
-                                t = resets ? fade(ei, t) : ei * t;
-                                v[i] = F16 ? fmaf(__uint_as_float(y[e][x + i]), back, t) : __uint_as_float(y[e][x + i]) + t;
-                            }
-                            w8[x / 2] = pack2<T>(v[0], v[1]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            *reinterpret_cast<uint4*>(row + (((2 * (u & 3) + i) ^ (r & 7)) * 16)) =
-                                make_uint4(w8[4 * i], w8[4 * i + 1], w8[4 * i + 2], w8[4 * i + 3]);
-                    }
-                tc::tc_fence_before();
-                tc::mbar_arrive(&s.o_free);
-                if (c < nc) {
-                    tc::fence_proxy_async_smem();
-                    tc::mbar_arrive(&s.o_staged);
-                } else if (p * CQ + r < len) {
-                    T* orow = static_cast<T*>(a.o) + (start + (long long)p * CQ + r) * a.ldo + (long long)h * a.dv + c0;
-#pragma unroll 1
-                    for (int e = 0; e < DV / 8; ++e)
-                        *reinterpret_cast<uint4*>(orow + 8 * e) = *reinterpret_cast<const uint4*>(
-                            (e < 8 ? s.q[b] : s.k[b]) + r * 128 + (((e & 7) ^ (r & 7)) * 16));
+                    for (int e = 0; e < 32; ++e) y[e] = dec0 == 0.f ? 0.f : y[e] * dec;
+                    tc::tmem_st32(dc + u, *reinterpret_cast<uint32_t(*)[32]>(&y));
                 }
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&s.tab_empty[p % NTAB]);
+                tc::tmem_wait_st();
             }
+            power = fk;
+            tc::fence_proxy_async_smem();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&s.s_ready);
+            scaled_keys<T, PARTS>(s.ks, krow, r, w * fk);
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(&s.k_ready);
         }
         wait(&s.d_done, (nc - 1) & 1, nc, 33);
         if (ok && mine && a.state_out && !*reinterpret_cast<volatile int*>(&s.dirty)) {
@@ -774,6 +681,84 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         make_float4(y[e] * back, y[e + 1] * back, y[e + 2] * back, y[e + 3] * back);
             }
         }
+    } else {
+        // ---------------- o: row r of the chunk ----------------
+        const int quad = warp & 3, r = quad * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        const uint32_t oc = tmem + lane_base + TM_O, o2c = tmem + lane_base + TM_O2;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t ph, int c, int id) {
+            if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(bar, ph, abort, wlim))) {
+                if (lane == 0) fail(abort, status, 2, c, id);
+                ok = false;
+            }
+        };
+        for (int c = 0; ok && c < nc; ++c) {
+            const int b = c & 1;
+            wait(&s.tab_full[c % NTAB], (c / NTAB) & 1, c, 35);
+            if (!ok) break;
+            const float ei = s.tab[c % NTAB].e[r];
+            const bool resets = s.tab[c % NTAB].resets;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&s.tab_empty[c % NTAB]);
+            wait(&s.o_full, c & 1, c, 38);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const float back = F16 ? inverse(s.ps[b][r]) : 1.f;
+            const float2 e2 = make_float2(ei, ei), back2 = make_float2(back, back);
+            // 32 columns at a time: the warp's 32 rows to shared memory, then 64-byte pieces of rows out
+            uint8_t* mid = s.mid[quad];
+            T* orow = static_cast<T*>(a.o) + (start + (long long)c * CQ + r - lane + (lane >> 2)) * a.ldo +
+                      (long long)h * a.dv + c0 + 8 * (lane & 3);
+            const int n = len - c * CQ - quad * 32 - (lane >> 2);  // rows from the lane's first to the sequence's end
+            uint32_t y[2][16], z[2][16];
+            tc::tmem_ld16(oc, y[0]);
+            tc::tmem_ld16(o2c, z[0]);
+#pragma unroll 1
+            for (int u0 = 0; u0 < DV / 16; u0 += 2) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int u = u0 + e;
+                    tc::tmem_wait_ld();
+                    if (u + 1 < DV / 16) {
+                        tc::tmem_ld16(oc + 16 * (u + 1), y[e ^ 1]);
+                        tc::tmem_ld16(o2c + 16 * (u + 1), z[e ^ 1]);
+                    }
+                    if (resets && ei == 0.f) {
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) z[e][x] = 0u;
+                    }
+                    uint32_t w8[8];
+#pragma unroll
+                    for (int x = 0; x < 16; x += 2) {
+                        float2 p = make_float2(__uint_as_float(y[e][x]), __uint_as_float(y[e][x + 1]));
+                        float2 t = make_float2(__uint_as_float(z[e][x]), __uint_as_float(z[e][x + 1]));
+                        if (F16) {
+                            p = __fmul2_rn(p, back2);
+                            t = __fmul2_rn(t, *reinterpret_cast<const float2*>(&s.col[b][16 * u + x]));
+                        }
+                        const float2 v = __ffma2_rn(t, e2, p);
+                        w8[x / 2] = pack2<T>(v.x, v.y);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        *reinterpret_cast<uint4*>(mid + lane * 64 + (((2 * e + i) ^ ((lane >> 1) & 3)) * 16)) =
+                            make_uint4(w8[4 * i], w8[4 * i + 1], w8[4 * i + 2], w8[4 * i + 3]);
+                }
+                if (u0 + 2 == DV / 16) {
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(&s.o_free);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int row = 8 * x + (lane >> 2);
+                    const uint4 w = *reinterpret_cast<const uint4*>(mid + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) * 16));
+                    if (8 * x < n) *reinterpret_cast<uint4*>(orow + 8 * x * a.ldo + 16 * u0) = w;
+                }
+                __syncwarp();
+            }
+        }
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -787,11 +772,10 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 template <typename T, int DV>
 int launch_dv(const Ctx& ctx, const LinAttn& x) {
     constexpr bool BF16 = std::is_same<T, bf16>::value;
-    CUtensorMap tq, tk, tv, to;
+    CUtensorMap tq, tk, tv;
     if (!tc::make_tmap_2d(&tq, x.q, BF16, x.total, (uint64_t)x.Hk * DK, x.ldq, CQ) ||
         !tc::make_tmap_2d(&tk, x.k, BF16, x.total, (uint64_t)x.Hk * DK, x.ldk, CQ) ||
-        !tc::make_tmap_2d(&tv, x.v, BF16, x.total, (uint64_t)x.H * x.dv, x.ldv, CQ) ||
-        !tc::make_tmap_2d(&to, x.o, BF16, x.total, (uint64_t)x.H * x.dv, x.ldo, CQ))
+        !tc::make_tmap_2d(&tv, x.v, BF16, x.total, (uint64_t)x.H * x.dv, x.ldv, CQ))
         return HYMBA_ERR_UNSUPPORTED;
     auto kern = linattn_tc_kernel<T, DV>;
     const size_t smem = sizeof(TcSmem<BF16 ? 3 : 2>) + 1024;
@@ -810,7 +794,7 @@ int launch_dv(const Ctx& ctx, const LinAttn& x) {
         a.cu = x.cu + s0;
         a.total = x.total; a.Hk = x.Hk; a.H = x.H; a.dv = x.dv;
         a.log2_scale = log2f(x.scale);
-        HYMBA_LAUNCH(ctx, "linattn_chunk", kern, dim3(x.dv / DV, x.H, n), NT, smem, tq, tk, tv, to, a, ctx.status);
+        HYMBA_LAUNCH(ctx, "linattn_chunk", kern, dim3(x.dv / DV, x.H, n), NT, smem, tq, tk, tv, a, ctx.status);
     }
     return HYMBA_OK;
 }
