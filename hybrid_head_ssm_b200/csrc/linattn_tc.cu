@@ -71,10 +71,12 @@ struct TcSmem {
     alignas(1024) uint8_t s16[2][TILE];     // the state's copy, rows = values
     alignas(128) uint8_t mid[4][32 * 64];   // o of each warp on its way out, 32 columns at a time
     Tables tab[NTAB];
-    float col[2][CQ];  // fp16: 1 / power of two of the copy's rows
+    // fp16: 1 / power of two of the copy's rows. Three: chunk c's are read until o_free(c), and the
+    // state of chunk c + 2 may be written before that, of c + 3 not
+    float col[3][CQ];
     float ps[2][CQ];   // fp16: the power of two of P's rows
     float kmax[2][4];
-    uint64_t full[2], v_ok[2], tab_full[NTAB], tab_empty[NTAB];
+    uint64_t full[2], empty[2], v_ok[2], tab_full[NTAB], tab_empty[NTAB];
     uint64_t s1_full, p_full, o_full, o_free, s_ready, k_ready, k_max, d_done, drain;
     uint32_t tmem_base;
     int abort, dirty;
@@ -277,6 +279,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&s.full[i], 1);
+            tc::mbar_init(&s.empty[i], 1);
             tc::mbar_init(&s.v_ok[i], 32);
         }
         for (int i = 0; i < NTAB; ++i) {
@@ -333,7 +336,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             for (int c = 0; c < nc; ++c) {
                 const int b = c & 1;
                 // the stage's chunk is done with its last product, which follows every read of it
-                if (c > 1 && !tc::mbar_wait(&s.o_full, c & 1, abort, wlim)) { fail(abort, status, 0, c, 1); break; }
+                if (!tc::mbar_wait(&s.empty[b], ((c >> 1) & 1) ^ 1, abort, wlim)) { fail(abort, status, 0, c, 1); break; }
                 tc::mbar_arrive_expect_tx(&s.full[b], (2 + DV / 64) * TILE);
                 tc::tma_load_2d(s.q[b], &tmQ, &s.full[b], hk * DK, start + c * CQ);
                 tc::tma_load_2d(s.k[b], &tmK, &s.full[b], hk * DK, start + c * CQ);
@@ -396,6 +399,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 for (int kk = 0; kk < CQ / 16; ++kk)
                     mma_f16_ts(tmem + TM_O, tmem + TM_S1 + kk * 8, tc::sdesc_mn_sw128(va + kk * 2048, TILE), ID_O, kk > 0);
                 tc::mma_commit(&s.o_full);
+                tc::mma_commit(&s.empty[b]);
             }
             // every MMA issued has completed before the block exits
             tc::mma_commit(&s.drain);
@@ -637,7 +641,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         for (int e = 0; e < 32; e += 2) m = fmax3(m, fabsf(y[e]), fabsf(y[e + 1]));
                     }
                     fs = to_middle(m, -100, 100);
-                    s.col[b][r] = inverse(fs) * inverse(power);
+                    s.col[c % 3][r] = inverse(fs) * inverse(power);
                     dec = dec0 * (fk * inverse(power));
                 }
                 uint8_t* row = s.s16[b] + r * 128;
@@ -735,7 +739,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         float2 t = make_float2(__uint_as_float(z[e][x]), __uint_as_float(z[e][x + 1]));
                         if (F16) {
                             p = __fmul2_rn(p, back2);
-                            t = __fmul2_rn(t, *reinterpret_cast<const float2*>(&s.col[b][16 * u + x]));
+                            t = __fmul2_rn(t, *reinterpret_cast<const float2*>(&s.col[c % 3][16 * u + x]));
                         }
                         const float2 v = __ffma2_rn(t, e2, p);
                         w8[x / 2] = pack2<T>(v.x, v.y);
