@@ -6,11 +6,13 @@
 // One CTA per (256 query rows of a sequence, head): two 128-row tiles that share every K
 // and V block of 128 keys and run as two pipelines, so that the tensor cores work on one
 // tile while the other tile's softmax runs. 12 warps:
-//   warp 0      lane 0: TMA of the two Q tiles and of the K blocks (ring);
-//   warp 1      TMEM, and one thread that issues every MMA, the tiles in turn: O_t += P_t V
-//               once the softmax stored P_t over S_t in TMEM, then, that product done, the
-//               next S_t = Q_t K^T into the same columns;
-//   warp 2      lane 0: TMA of the V blocks (ring);
+//   warp 0      one lane: TMA of the two Q tiles and of the K and V blocks (rings);
+//   warps 1, 2  one thread each that issues the products of tile A, B in steps of 64 keys: O_t
+//               += P_t V once the softmax stored P_t over its scores in TMEM, then, that product
+//               done, the scores S_t = Q_t K^T two steps on into the same columns. The other half
+//               of the tile's columns holds the step between, so that the softmax goes from
+//               step to step without waiting for a product. (One thread for both tiles could
+//               not issue as fast as the softmax went: 969 us against the figure below.)
 //   warp 3      looks at the V blocks that hold keys some row does not see: rows behind
 //               the sequence become zero (they belong to another sequence, and 0 x NaN
 //               would reach the product), and a value that is not finite is replaced by 0
@@ -31,6 +33,7 @@ namespace hymba {
 namespace {
 
 constexpr int QT = 128, KB = 128;
+constexpr int KS = 64;  // keys per softmax step: half a block
 constexpr int NT = 384;
 constexpr int REG_SOFT = 216, REG_OTHER = 64;
 // the launch allocates 168 registers per thread (65536 / 384, rounded down to 8): the
@@ -53,7 +56,7 @@ struct PackedSmem {
     uint64_t q_full;
     uint64_t k_full[ST], k_empty[ST];
     uint64_t v_full[ST], v_ok[ST], v_empty[ST];
-    uint64_t s_full[2], p_full[2], pv_done[2], drain;
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_done[2];
     uint32_t tmem_base;
     int abort, dirty;
     ragged::FindSmem find;
@@ -105,15 +108,31 @@ __device__ __forceinline__ void fail(volatile int* abort, int* status, int role,
     tc::record_timeout(status, role, step, bar);
 }
 
-// 16 bytes of 16-bit values: nonzero if one is infinite or NaN (its exponent bits all set)
-template <bool BF16>
-__device__ __forceinline__ uint32_t odd16(uint4 x) {
-    constexpr uint32_t E = BF16 ? 0x7f807f80u : 0x7c007c00u;
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t r = 0;
+// Whether the lane's share of PIECES 16-byte pieces holds a value that is infinite or NaN: 0 x it
+// is NaN, and a sum of such products stays NaN. Eight loads in flight: one at a time, a block
+// of V took longer to look through than its softmax.
+template <bool BF16, int PIECES>
+__device__ __forceinline__ bool any_odd(const uint4* v, int lane) {
+    typedef typename std::conditional<BF16, __nv_bfloat162, __half2>::type P2;
+    const uint32_t nul = 0u;
+    uint32_t acc[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+    for (int x = lane; x < PIECES; x += 32 * 8) {
+        uint4 w[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r |= __vcmpeq2(w[i] & E, E);
-    return r;
+        for (int y = 0; y < 8; ++y) w[y] = v[x + 32 * y];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+            const uint32_t ww[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const P2 r = __hfma2(*reinterpret_cast<const P2*>(&ww[i]), *reinterpret_cast<const P2*>(&nul),
+                                     *reinterpret_cast<const P2*>(&acc[i]));
+                acc[i] = *reinterpret_cast<const uint32_t*>(&r);
+            }
+        }
+    }
+    return ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0;
 }
 template <bool BF16>
 __device__ __forceinline__ uint32_t drop_odd(uint32_t w) {
@@ -166,7 +185,7 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     extern __shared__ uint8_t smem_raw[];
     PackedSmem<DH, DV>& s = *reinterpret_cast<PackedSmem<DH, DV>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                                  ~static_cast<uintptr_t>(1023));
-    constexpr uint32_t IDESC_S = tc::idesc_f16(BF16, QT, KB);
+    constexpr uint32_t IDESC_S = tc::idesc_f16(BF16, QT, KS);
     constexpr uint32_t IDESC_PV = tc::idesc_f16(BF16, QT, DV, true);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -180,11 +199,13 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
             tc::mbar_init(&s.v_empty[i], 2);
         }
         for (int t = 0; t < 2; ++t) {
-            tc::mbar_init(&s.s_full[t], 1);
-            tc::mbar_init(&s.p_full[t], QT);
+            for (int x = 0; x < 2; ++x) {
+                tc::mbar_init(&s.s_full[t][x], 1);
+                tc::mbar_init(&s.p_full[t][x], QT);
+            }
             tc::mbar_init(&s.pv_done[t], 1);
+            tc::mbar_init(&s.o_done[t], 1);
         }
-        tc::mbar_init(&s.drain, 1);
         s.abort = 0;
         s.dirty = 0;
         tc::fence_mbar_init();
@@ -219,9 +240,9 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     if (warp < 4) {
         setmaxnreg_dec<REG_OTHER>();
         if (warp == 0) {
-            // ---------------- TMA: Q, K ----------------
+            // ---------------- TMA ----------------
             if (lane == 0) {
-                int issued = 0;
+                int k_issued = 0, v_issued = 0;
                 tc::mbar_arrive_expect_tx(&s.q_full, 2 * QT * DH * 2);
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
@@ -229,94 +250,90 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                     for (int p = 0; p < DH / 64; ++p)
                         tc::tma_load_2d(s.q[t][p], &tmQ, &s.q_full, h * DH + p * 64, it.start + i0 + t * QT);
                 for (int j = 0; j < nblk; ++j) {
-                    const int st = j % ST;
+                    const int st = j % ST, key = it.start + blk.key0(j);
                     if (!tc::mbar_wait(&s.k_empty[st], ((j / ST) & 1) ^ 1, abort, wlim)) { fail(abort, status, 0, j, 1); break; }
                     tc::mbar_arrive_expect_tx(&s.k_full[st], KB * DH * 2);
 #pragma unroll
                     for (int p = 0; p < DH / 64; ++p)
-                        tc::tma_load_2d(s.k[st][p], &tmK, &s.k_full[st], g * DH + p * 64, it.start + blk.key0(j));
-                    issued = j + 1;
-                }
-                // every copy issued has landed before the block exits
-                tc::mbar_wait(&s.q_full, 0, &zero);
-                for (int j = max(0, issued - ST); j < issued; ++j) tc::mbar_wait(&s.k_full[j % ST], (j / ST) & 1, &zero);
-            }
-        } else if (warp == 1) {
-            // ---------------- MMA issuer ----------------
-            if (tc::elect_one()) {
-                bool ok = tc::mbar_wait(&s.q_full, 0, abort, wlim);
-                if (!ok) fail(abort, status, 1, 0, 0);
-                const int nA = blk.A.count(), nB = blk.B.count();
-                // S_t(u) = Q_t K^T; frees the K stage (two commits when the other tile skips it)
-                auto issue_s = [&](int t, int u) -> bool {
-                    const int j = t ? blk.B.nth(u) : blk.A.nth(u), st = j % ST;
-                    if (!tc::mbar_wait(&s.k_full[st], (j / ST) & 1, abort, wlim)) { fail(abort, status, 1, j, 2); return false; }
-                    tc::tc_fence_after();
-                    const uint32_t sd = tmem + TM_S + t * 128;
-#pragma unroll
-                    for (int p = 0; p < DH / 64; ++p) {
-                        const uint32_t qa = tc::smem_u32(s.q[t][p]), ka = tc::smem_u32(s.k[st][p]);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc::mma_f16_ss(sd, tc::sdesc_k_sw128(qa + kk * 32), tc::sdesc_k_sw128(ka + kk * 32), IDESC_S,
-                                           p > 0 || kk > 0);
-                    }
-                    tc::mma_commit(&s.s_full[t]);
-                    tc::mma_commit(&s.k_empty[st]);
-                    if (!blk.shared(j)) tc::mma_commit(&s.k_empty[st]);
-                    return true;
-                };
-                // O_t += P_t V, P_t read from TMEM (the tile's S columns)
-                auto issue_pv = [&](int t, int u) -> bool {
-                    const int j = t ? blk.B.nth(u) : blk.A.nth(u), st = j % ST;
-                    if (!tc::mbar_wait(&s.v_ok[st], (j / ST) & 1, abort, wlim)) { fail(abort, status, 1, j, 10); return false; }
-                    if (!tc::mbar_wait(&s.p_full[t], u & 1, abort, wlim)) { fail(abort, status, 1, j, 4 + t); return false; }
-                    tc::tc_fence_after();
-                    const uint32_t va = tc::smem_u32(s.v[st][0]);
-                    const uint32_t pa = tmem + TM_S + t * 128;
-#pragma unroll
-                    for (int kk = 0; kk < KB / 16; ++kk)
-                        mma_f16_ts(tmem + TM_O + t * 128, pa + kk * 8, tc::sdesc_mn_sw128(va + kk * 2048, KB * 128), IDESC_PV,
-                                   u > 0 || kk > 0);
-                    tc::mma_commit(&s.pv_done[t]);
-                    tc::mma_commit(&s.v_empty[st]);
-                    if (!blk.shared(j)) tc::mma_commit(&s.v_empty[st]);
-                    return true;
-                };
-                if (ok && nA > 0) ok = issue_s(0, 0);
-                if (ok && nB > 0) ok = issue_s(1, 0);
-                const int n_max = max(nA, nB);
-                for (int u = 0; ok && u < n_max; ++u)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int n = t ? nB : nA;
-                        if (!ok || u >= n) continue;
-                        ok = issue_pv(t, u);
-                        if (ok && u + 1 < n) {
-                            // the next S overwrites P
-                            ok = tc::mbar_wait(&s.pv_done[t], u & 1, abort, wlim);
-                            if (!ok) fail(abort, status, 1, u, 11);
-                            else ok = issue_s(t, u + 1);
-                        }
-                    }
-                // every MMA issued has completed before the block exits
-                tc::mma_commit(&s.drain);
-                tc::mbar_wait(&s.drain, 0, &zero);
-            }
-        } else if (warp == 2) {
-            // ---------------- TMA: V ----------------
-            if (lane == 0) {
-                int issued = 0;
-                for (int j = 0; j < nblk; ++j) {
-                    const int st = j % ST;
+                        tc::tma_load_2d(s.k[st][p], &tmK, &s.k_full[st], g * DH + p * 64, key);
+                    k_issued = j + 1;
                     if (!tc::mbar_wait(&s.v_empty[st], ((j / ST) & 1) ^ 1, abort, wlim)) { fail(abort, status, 0, j, 9); break; }
                     tc::mbar_arrive_expect_tx(&s.v_full[st], KB * DV * 2);
 #pragma unroll
                     for (int p = 0; p < DV / 64; ++p)
-                        tc::tma_load_2d(s.v[st][p], &tmV, &s.v_full[st], g * DV + p * 64, it.start + blk.key0(j));
-                    issued = j + 1;
+                        tc::tma_load_2d(s.v[st][p], &tmV, &s.v_full[st], g * DV + p * 64, key);
+                    v_issued = j + 1;
                 }
-                for (int j = max(0, issued - ST); j < issued; ++j) tc::mbar_wait(&s.v_full[j % ST], (j / ST) & 1, &zero);
+                // every copy issued has landed before the block exits
+                tc::mbar_wait(&s.q_full, 0, &zero);
+                for (int j = max(0, k_issued - ST); j < k_issued; ++j) tc::mbar_wait(&s.k_full[j % ST], (j / ST) & 1, &zero);
+                for (int j = max(0, v_issued - ST); j < v_issued; ++j) tc::mbar_wait(&s.v_full[j % ST], (j / ST) & 1, &zero);
+            }
+        } else if (warp < 3) {
+            // ---------------- MMA issuer of tile t ----------------
+            if (tc::elect_one()) {
+                const int t = warp - 1;
+                const Use use = t ? blk.B : blk.A;
+                const int n = 2 * use.count();  // steps of 64 keys
+                bool ok = true;
+                auto wait = [&](uint64_t* bar, uint32_t ph, int k, int id) {
+                    if (ok && !tc::mbar_wait(bar, ph, abort, wlim)) {
+                        fail(abort, status, 1, k, id);
+                        ok = false;
+                    }
+                };
+                const uint64_t qd = tc::sdesc_k_sw128(tc::smem_u32(s.q[t][0])), kd = tc::sdesc_k_sw128(tc::smem_u32(s.k[0][0]));
+                const uint64_t vd = tc::sdesc_mn_sw128(tc::smem_u32(s.v[0][0]), KB * 128);
+                const uint32_t sd = tmem + TM_S + t * 128, od = tmem + TM_O + t * 128;
+                // step k: half k % 2 of the tile's block k / 2; its scores, and P over them, in half k % 2
+                // of the tile's S columns.
+                // S_t(k) = Q_t K^T; the second half frees the K stage (two commits when the other
+                // tile skips the block)
+                auto issue_s = [&](int k) {
+                    const int j = use.nth(k >> 1), st = j % ST, x = k & 1;
+                    if (x == 0) wait(&s.k_full[st], (j / ST) & 1, j, 2);
+                    if (!ok) return;
+                    tc::tc_fence_after();
+                    const uint64_t kx = kd + (uint64_t)(st * (DH / 64) * (KB * 128 / 16) + x * (KS * 128 / 16));
+#pragma unroll
+                    for (int p = 0; p < DH / 64; ++p)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc::mma_f16_ss(sd + x * KS, qd + p * (QT * 128 / 16) + kk * 2, kx + p * (KB * 128 / 16) + kk * 2,
+                                           IDESC_S, p > 0 || kk > 0);
+                    tc::mma_commit(&s.s_full[t][x]);
+                    if (x) {
+                        tc::mma_commit(&s.k_empty[st]);
+                        if (!blk.shared(j)) tc::mma_commit(&s.k_empty[st]);
+                    }
+                };
+                wait(&s.q_full, 0, 0, 0);
+                for (int k = 0; k < min(n, 2); ++k) issue_s(k);
+                for (int k = 0; ok && k < n; ++k) {
+                    // O_t += P_t V, P_t read from TMEM
+                    const int j = use.nth(k >> 1), st = j % ST, x = k & 1;
+                    if (x == 0) wait(&s.v_ok[st], (j / ST) & 1, j, 10);
+                    wait(&s.p_full[t][x], (k >> 1) & 1, j, 4);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const uint64_t vx = vd + (uint64_t)(st * (DV / 64) * (KB * 128 / 16) + x * (KS * 128 / 16));
+#pragma unroll
+                    for (int kk = 0; kk < KS / 16; ++kk)
+                        mma_f16_ts(od, sd + x * KS + kk * 8, vx + kk * (2048 / 16), IDESC_PV, k > 0 || kk > 0);
+                    tc::mma_commit(&s.pv_done[t]);
+                    if (x) {
+                        tc::mma_commit(&s.v_empty[st]);
+                        if (!blk.shared(j)) tc::mma_commit(&s.v_empty[st]);
+                    }
+                    // the scores two steps on take the columns of this P
+                    if (k + 2 < n) {
+                        wait(&s.pv_done[t], k & 1, k, 11);
+                        if (ok) issue_s(k + 2);
+                    }
+                }
+                // every MMA issued has completed: the tile's O is whole, and the block may exit
+                tc::mma_commit(&s.o_done[t]);
+                tc::mbar_wait(&s.o_done[t], 0, &zero);
             }
         } else {
             // ---------------- V blocks with keys that some row does not see ----------------
@@ -332,24 +349,20 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 const bool whole = j < blk.nmb ? k0 + KB <= min(n_meta, i0 + 1)
                                                : k0 + KB <= i0 + 1 && (window <= 0 || last - k0 < window);
                 if (!whole) {
-                    uint8_t* vb = s.v[st][0];
-                    uint32_t odd = 0;
                     // 16-byte piece x of panel p: row x / 8 (the swizzle moves pieces within a row)
-                    for (int x = lane; x < KB * 8 * (DV / 64); x += 32) {
-                        const int row = (x >> 3) & (KB - 1);
-                        uint4* at = reinterpret_cast<uint4*>(vb + x * 16);
-                        if (k0 + row >= L) *at = make_uint4(0, 0, 0, 0);
-                        else odd |= odd16<BF16>(*at);
-                    }
-                    if (__any_sync(0xffffffffu, odd != 0)) {
-                        for (int x = lane; x < KB * 8 * (DV / 64); x += 32) {
-                            uint4* at = reinterpret_cast<uint4*>(vb + x * 16);
-                            uint4 w = *at;
+                    uint4* vb = reinterpret_cast<uint4*>(s.v[st][0]);
+                    constexpr int PIECES = KB * 8 * (DV / 64);
+                    if (k0 + KB > L)
+                        for (int x = lane; x < PIECES; x += 32)
+                            if (k0 + ((x >> 3) & (KB - 1)) >= L) vb[x] = make_uint4(0, 0, 0, 0);
+                    if (__any_sync(0xffffffffu, any_odd<BF16, PIECES>(vb, lane))) {
+                        for (int x = lane; x < PIECES; x += 32) {
+                            uint4 w = vb[x];
                             w.x = drop_odd<BF16>(w.x);
                             w.y = drop_odd<BF16>(w.y);
                             w.z = drop_odd<BF16>(w.z);
                             w.w = drop_odd<BF16>(w.w);
-                            *at = w;
+                            vb[x] = w;
                         }
                         if (lane == 0) *reinterpret_cast<volatile int*>(&s.dirty) = 1;
                     }
@@ -373,47 +386,46 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         const int wa = window > 0 ? max(n_meta, i - window + 1) : n_meta;
         float m_used = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int u = 0; u < nt; ++u) {
+        for (int k = 0; k < 2 * nt; ++k) {
+            const int x = k & 1;
             // tcgen05.ld/st are warp-collective: every decision that guards them is taken
             // by the whole warp (__all_sync / __any_sync)
-            if (!__all_sync(0xffffffffu, tc::mbar_wait(&s.s_full[t], u & 1, abort, wlim))) {
-                if (lane == 0) fail(abort, status, 2, u, 5);
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(&s.s_full[t][x], (k >> 1) & 1, abort, wlim))) {
+                if (lane == 0) fail(abort, status, 2, k, 5);
                 ok = false;
                 break;
             }
             tc::tc_fence_after();
-            // the four 32-column loads in flight together, one wait
-            uint32_t sr[4][32];
+            // the two 32-column loads in flight together, one wait
+            uint32_t sr[2][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_cols + c * 32, sr[c]);
+            for (int c = 0; c < 2; ++c) tc::tmem_ld32(s_cols + x * KS + c * 32, sr[c]);
             tc::tmem_wait_ld();
             float* sv = reinterpret_cast<float*>(&sr[0][0]);
-            // mask: the keys row i sees in this block form one interval [ka, ke)
-            const int j = use.nth(u), k0 = blk.key0(j);
+            // mask: the keys row i sees in this step form one interval [ka, ke)
+            const int j = use.nth(k >> 1), k0 = blk.key0(j) + x * KS;
             const bool meta_blk = j < blk.nmb;
             const int ka = meta_blk ? 0 : wa;
             const int ke = meta_blk ? meta_e : i + 1;
-            if (ka > k0 || ke < k0 + KB) {
+            if (ka > k0 || ke < k0 + KS) {
                 const unsigned span = ke > ka ? (unsigned)(ke - ka) : 0u;
 #pragma unroll
-                for (int c = 0; c < 128; ++c) sv[c] = (unsigned)(k0 + c - ka) < span ? sv[c] : -INFINITY;
+                for (int c = 0; c < KS; ++c) sv[c] = (unsigned)(k0 + c - ka) < span ? sv[c] : -INFINITY;
             }
-            // row max with three-input max: 8 independent chains over the 128 scores
+            // row max with three-input max: 8 independent chains over the 64 scores
             float mx8[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) mx8[c] = fmax3(sv[c], sv[c + 8], sv[c + 16]);
 #pragma unroll
-            for (int c = 24; c + 16 < 128; c += 16)
+            for (int c = 24; c + 16 <= KS; c += 16)
 #pragma unroll
-                for (int x = 0; x < 8; ++x) mx8[x] = fmax3(mx8[x], sv[c + x], sv[c + 8 + x]);
+                for (int y = 0; y < 8; ++y) mx8[y] = fmax3(mx8[y], sv[c + y], sv[c + 8 + y]);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) mx8[x] = fmaxf(mx8[x], sv[120 + x]);
+            for (int y = 0; y < 8; ++y) mx8[y] = fmaxf(mx8[y], sv[KS - 8 + y]);
             const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                                    fmaxf(mx8[6], mx8[7])) * scale;
-            // a row whose running max grows by more than 2^8 moves to the new max; its O
-            // (PV of the earlier blocks, all completed: this S was issued after the last
-            // PV of the tile completed) is scaled in TMEM once P is stored (before the PV
-            // of this block is released)
+            // a row whose running max grows by more than 2^8 moves to the new max, and its O is
+            // scaled in TMEM, between the products of the step before and of this one
             float f = 1.f;
             bool scale_o = false;
             if (mx > m_used + RESCALE_LOG2) {
@@ -427,47 +439,59 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
             // P = 2^(s * scale - m) in fp32, summed in fp32, stored as 16-bit pairs
             const float mu = m_used == -INFINITY ? 0.f : m_used;
             const float2 sc2 = make_float2(scale, scale), nmu2 = make_float2(-mu, -mu);
-            uint32_t pk[64];
+            uint32_t pk[32];
             float2 l4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
-                const float2 x = __ffma2_rn(make_float2(sv[2 * c], sv[2 * c + 1]), sc2, nmu2);
-                const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            for (int c = 0; c < KS / 2; ++c) {
+                const float2 y = __ffma2_rn(make_float2(sv[2 * c], sv[2 * c + 1]), sc2, nmu2);
+                const float2 p = make_float2(fast_exp2(y.x), fast_exp2(y.y));
                 l4[c & 3] = __fadd2_rn(l4[c & 3], p);
                 pk[c] = pack2<T>(p.x, p.y);
             }
             const float2 l2 = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
             l += l2.x + l2.y;
-            tmem_st64(s_cols, pk);
+            tc::tmem_st32(s_cols + x * KS, pk);
             tc::tmem_wait_st();
             if (__any_sync(0xffffffffu, scale_o)) {
-                uint32_t rr[DV / 32][32];
-#pragma unroll
-                for (int c = 0; c < DV / 32; ++c) tc::tmem_ld32(o_cols + c * 32, rr[c]);
-                tc::tmem_wait_ld();
+                // (the product of this step waits for this thread; that of the step before may still run)
+                if (!__all_sync(0xffffffffu, tc::mbar_wait(&s.pv_done[t], (k - 1) & 1, abort, wlim))) {
+                    if (lane == 0) fail(abort, status, 2, k, 6);
+                    ok = false;
+                    break;
+                }
+                tc::tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < DV / 32; ++c) {
+                    uint32_t rr[32];
+                    tc::tmem_ld32(o_cols + c * 32, rr);
+                    tc::tmem_wait_ld();
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) rr[c][x] = __float_as_uint(__uint_as_float(rr[c][x]) * f);
-                    tc::tmem_st32(o_cols + c * 32, rr[c]);
+                    for (int y = 0; y < 32; ++y) rr[y] = __float_as_uint(__uint_as_float(rr[y]) * f);
+                    tc::tmem_st32(o_cols + c * 32, rr);
                 }
                 tc::tmem_wait_st();
             }
             tc::tc_fence_before();
-            tc::mbar_arrive(&s.p_full[t]);
+            tc::mbar_arrive(&s.p_full[t][x]);
         }
-        if (ok && nt > 0 && __all_sync(0xffffffffu, tc::mbar_wait(&s.pv_done[t], (nt - 1) & 1, abort, wlim))) {
+        if (ok && nt > 0 && __all_sync(0xffffffffu, tc::mbar_wait(&s.o_done[t], 0, abort, wlim))) {
             tc::tc_fence_after();
             // no visible score above -infinity: zeros; a NaN sum divides, so that a visible NaN
             // reaches its row
             const float inv = l == 0.f ? 0.f : 1.f / l;
             T* orow = static_cast<T*>(a.o) + (it.start + (long long)i) * a.ldo + (long long)h * DV;
+            // 64 columns at a time through the tile's Q (no longer needed): the warp's 32 rows there,
+            // then whole 128-byte pieces of rows out
+            uint8_t* mid = s.q[t][0] + q * 4096;
+            T* out = orow - (long long)lane * a.ldo;  // the warp's first row
+            const int n = L - i + lane;               // rows from there to the sequence's end
 #pragma unroll 1
-            for (int c = 0; c < DV / 32; ++c) {
-                uint32_t rr[32];
-                tc::tmem_ld32(o_cols + c * 32, rr);
-                tc::tmem_wait_ld();
-                if (i < L) {
+            for (int v0 = 0; v0 < DV; v0 += 64) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t rr[32];
+                    tc::tmem_ld32(o_cols + v0 + c * 32, rr);
+                    tc::tmem_wait_ld();
 #pragma unroll
                     for (int x = 0; x < 32; x += 8) {
                         uint4 pk;
@@ -475,9 +499,17 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                         pk.y = pack2<T>(__uint_as_float(rr[x + 2]) * inv, __uint_as_float(rr[x + 3]) * inv);
                         pk.z = pack2<T>(__uint_as_float(rr[x + 4]) * inv, __uint_as_float(rr[x + 5]) * inv);
                         pk.w = pack2<T>(__uint_as_float(rr[x + 6]) * inv, __uint_as_float(rr[x + 7]) * inv);
-                        *reinterpret_cast<uint4*>(orow + c * 32 + x) = pk;
+                        *reinterpret_cast<uint4*>(mid + lane * 128 + (((4 * c + (x >> 3)) ^ (lane & 7)) * 16)) = pk;
                     }
                 }
+                __syncwarp();
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const int row = 4 * x + (lane >> 3), e = lane & 7;
+                    const uint4 w = *reinterpret_cast<const uint4*>(mid + row * 128 + ((e ^ (row & 7)) * 16));
+                    if (row < n) *reinterpret_cast<uint4*>(out + row * a.ldo + v0 + 8 * e) = w;
+                }
+                __syncwarp();
             }
             if (i < L && *reinterpret_cast<volatile int*>(&s.dirty))
                 recompute_row<T, DH, DV>(static_cast<const T*>(a.q) + (it.start + (long long)i) * a.ldq + (long long)h * DH,
