@@ -84,7 +84,6 @@ struct Use {
     __device__ int count() const { return mc + wn; }
     // the u-th block of the tile
     __device__ int nth(int u) const { return u < mc ? u : ws + (u - mc); }
-    __device__ bool uses(int j, int nmb) const { return j < nmb ? j < mc : j >= ws && j < ws + wn; }
 };
 struct Blocks {
     int nmb, lo, n;
@@ -100,7 +99,6 @@ struct Blocks {
         B.place(nmb, lo);
     }
     __device__ int key0(int j) const { return j < nmb ? j * KB : lo + (j - nmb) * KB; }
-    __device__ bool shared(int j) const { return A.uses(j, nmb) && B.uses(j, nmb); }
 };
 
 __device__ __forceinline__ void fail(volatile int* abort, int* status, int role, int step, int bar) {
@@ -193,7 +191,7 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         tc::mbar_init(&s.q_full, 1);
         for (int i = 0; i < ST; ++i) {
             tc::mbar_init(&s.k_full[i], 1);
-            tc::mbar_init(&s.k_empty[i], 2);  // one commit per tile (two for a block one tile skips)
+            tc::mbar_init(&s.k_empty[i], 2);  // the two tiles
             tc::mbar_init(&s.v_full[i], 1);
             tc::mbar_init(&s.v_ok[i], 32);
             tc::mbar_init(&s.v_empty[i], 2);
@@ -218,13 +216,6 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     griddep_sync();
     const ragged::Item it = ragged::find_item<NT>(s.find, a.cu, a.n_seqs, a.total, 2 * QT, false, blockIdx.x / a.H, status);
     if (it.seq < 0) return;
-    if (warp == 1) {
-        tc::tmem_alloc(&s.tmem_base, 512);
-        tc::tmem_relinquish();
-    }
-    tc::tc_fence_before();
-    __syncthreads();
-    tc::tc_fence_after();
     const int L = it.len;
     const int i0 = ((L + 2 * QT - 1) / (2 * QT) - 1 - it.tile) * 2 * QT;  // the heaviest rows first
     const int h = blockIdx.x % a.H, g = h / (a.H / a.G);
@@ -232,6 +223,26 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     Blocks blk;
     blk.init(i0, L, n_meta, window);
     const int nblk = blk.n;
+    if (threadIdx.x == 0 && nblk > 0) {
+        // (the thread that initialised the barriers; Q and the first K are on their way while TMEM is
+        // allocated)
+        tc::mbar_arrive_expect_tx(&s.q_full, 2 * QT * DH * 2);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int p = 0; p < DH / 64; ++p)
+                tc::tma_load_2d(s.q[t][p], &tmQ, &s.q_full, h * DH + p * 64, it.start + i0 + t * QT);
+        tc::mbar_arrive_expect_tx(&s.k_full[0], KB * DH * 2);
+#pragma unroll
+        for (int p = 0; p < DH / 64; ++p) tc::tma_load_2d(s.k[0][p], &tmK, &s.k_full[0], g * DH + p * 64, it.start + blk.key0(0));
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(&s.tmem_base, 512);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
     const uint32_t tmem = s.tmem_base;
     volatile int* abort = &s.abort;
     const long long wlim = tc::wait_limit(status);
@@ -243,19 +254,15 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
             // ---------------- TMA ----------------
             if (lane == 0) {
                 int k_issued = 0, v_issued = 0;
-                tc::mbar_arrive_expect_tx(&s.q_full, 2 * QT * DH * 2);
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int p = 0; p < DH / 64; ++p)
-                        tc::tma_load_2d(s.q[t][p], &tmQ, &s.q_full, h * DH + p * 64, it.start + i0 + t * QT);
                 for (int j = 0; j < nblk; ++j) {
                     const int st = j % ST, key = it.start + blk.key0(j);
                     if (!tc::mbar_wait(&s.k_empty[st], ((j / ST) & 1) ^ 1, abort, wlim)) { fail(abort, status, 0, j, 1); break; }
-                    tc::mbar_arrive_expect_tx(&s.k_full[st], KB * DH * 2);
+                    if (j > 0) {
+                        tc::mbar_arrive_expect_tx(&s.k_full[st], KB * DH * 2);
 #pragma unroll
-                    for (int p = 0; p < DH / 64; ++p)
-                        tc::tma_load_2d(s.k[st][p], &tmK, &s.k_full[st], g * DH + p * 64, key);
+                        for (int p = 0; p < DH / 64; ++p)
+                            tc::tma_load_2d(s.k[st][p], &tmK, &s.k_full[st], g * DH + p * 64, key);
+                    }
                     k_issued = j + 1;
                     if (!tc::mbar_wait(&s.v_empty[st], ((j / ST) & 1) ^ 1, abort, wlim)) { fail(abort, status, 0, j, 9); break; }
                     tc::mbar_arrive_expect_tx(&s.v_full[st], KB * DV * 2);
@@ -285,13 +292,31 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 const uint64_t qd = tc::sdesc_k_sw128(tc::smem_u32(s.q[t][0])), kd = tc::sdesc_k_sw128(tc::smem_u32(s.k[0][0]));
                 const uint64_t vd = tc::sdesc_mn_sw128(tc::smem_u32(s.v[0][0]), KB * 128);
                 const uint32_t sd = tmem + TM_S + t * 128, od = tmem + TM_O + t * 128;
+                // Both tiles take part in every phase of the rings, so that neither can be a phase
+                // ahead or behind: a block that the tile does not use is waited for and released.
+                int jk = 0, jv = 0;
+                auto pass_k = [&](int to) {
+                    for (; ok && jk < to; ++jk) {
+                        wait(&s.k_full[jk % ST], (jk / ST) & 1, jk, 2);
+                        tc::mbar_arrive(&s.k_empty[jk % ST]);
+                    }
+                };
+                auto pass_v = [&](int to) {
+                    for (; ok && jv < to; ++jv) {
+                        wait(&s.v_ok[jv % ST], (jv / ST) & 1, jv, 10);
+                        tc::mbar_arrive(&s.v_empty[jv % ST]);
+                    }
+                };
                 // step k: half k % 2 of the tile's block k / 2; its scores, and P over them, in half k % 2
                 // of the tile's S columns.
-                // S_t(k) = Q_t K^T; the second half frees the K stage (two commits when the other
-                // tile skips the block)
+                // S_t(k) = Q_t K^T; the second half frees the K stage
                 auto issue_s = [&](int k) {
                     const int j = use.nth(k >> 1), st = j % ST, x = k & 1;
-                    if (x == 0) wait(&s.k_full[st], (j / ST) & 1, j, 2);
+                    if (x == 0) {
+                        pass_k(j);
+                        wait(&s.k_full[st], (j / ST) & 1, j, 2);
+                        jk = j + 1;
+                    }
                     if (!ok) return;
                     tc::tc_fence_after();
                     const uint64_t kx = kd + (uint64_t)(st * (DH / 64) * (KB * 128 / 16) + x * (KS * 128 / 16));
@@ -302,17 +327,18 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                             tc::mma_f16_ss(sd + x * KS, qd + p * (QT * 128 / 16) + kk * 2, kx + p * (KB * 128 / 16) + kk * 2,
                                            IDESC_S, p > 0 || kk > 0);
                     tc::mma_commit(&s.s_full[t][x]);
-                    if (x) {
-                        tc::mma_commit(&s.k_empty[st]);
-                        if (!blk.shared(j)) tc::mma_commit(&s.k_empty[st]);
-                    }
+                    if (x) tc::mma_commit(&s.k_empty[st]);
                 };
                 wait(&s.q_full, 0, 0, 0);
                 for (int k = 0; k < min(n, 2); ++k) issue_s(k);
                 for (int k = 0; ok && k < n; ++k) {
                     // O_t += P_t V, P_t read from TMEM
                     const int j = use.nth(k >> 1), st = j % ST, x = k & 1;
-                    if (x == 0) wait(&s.v_ok[st], (j / ST) & 1, j, 10);
+                    if (x == 0) {
+                        pass_v(j);
+                        wait(&s.v_ok[st], (j / ST) & 1, j, 10);
+                        jv = j + 1;
+                    }
                     wait(&s.p_full[t][x], (k >> 1) & 1, j, 4);
                     if (!ok) break;
                     tc::tc_fence_after();
@@ -321,15 +347,17 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                     for (int kk = 0; kk < KS / 16; ++kk)
                         mma_f16_ts(od, sd + x * KS + kk * 8, vx + kk * (2048 / 16), IDESC_PV, k > 0 || kk > 0);
                     tc::mma_commit(&s.pv_done[t]);
-                    if (x) {
-                        tc::mma_commit(&s.v_empty[st]);
-                        if (!blk.shared(j)) tc::mma_commit(&s.v_empty[st]);
-                    }
+                    if (x) tc::mma_commit(&s.v_empty[st]);
                     // the scores two steps on take the columns of this P
                     if (k + 2 < n) {
                         wait(&s.pv_done[t], k & 1, k, 11);
                         if (ok) issue_s(k + 2);
                     }
+                }
+                // (block by block: the loads of K and V take turns)
+                for (int j = jv; ok && j < nblk; ++j) {
+                    pass_k(j + 1);
+                    pass_v(j + 1);
                 }
                 // every MMA issued has completed: the tile's O is whole, and the block may exit
                 tc::mma_commit(&s.o_done[t]);

@@ -35,6 +35,32 @@ template <int NT>
 __device__ Item find_item(FindSmem& sm, const int* cu, int n_seqs, int total, int rows, bool min_one, long long t,
                           int* status) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (n_seqs <= 32) {
+        // every warp for itself: one round trip, no barrier
+        int a = 0, n = 0, c = 0;
+        if (lane < n_seqs) {
+            if (sequence(cu, lane, total, &a, &n)) {
+                c = (n + rows - 1) / rows;
+                if (min_one && c == 0) c = 1;
+            } else if (blockIdx.x == 0 && warp == 0) {
+                set_status(status, HYMBA_ERR_DEVICE_RANGE);
+            }
+        }
+        long long incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, t >= incl - c && t < incl);
+        const int at = hit ? __ffs(hit) - 1 : 0;
+        Item it;
+        it.seq = hit ? at : -1;
+        it.start = __shfl_sync(0xffffffffu, a, at);
+        it.len = __shfl_sync(0xffffffffu, n, at);
+        it.tile = (int)(t - __shfl_sync(0xffffffffu, incl - c, at));
+        return it;
+    }
     const int per = (n_seqs + NT - 1) / NT;
     const int s0 = min(tid * per, n_seqs), s1 = min(s0 + per, n_seqs);
     if (tid == 0) sm.item.seq = -1;

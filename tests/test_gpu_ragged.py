@@ -98,6 +98,11 @@ PREFILL = [
     ([640], (5, 1), (64, 128), 200, 128),
     ([3, 2, 1, 1, 0, 0, 4], (4, 4), (64, 64), 2, 2),
     ([700], (2, 2), (128, 128), 0, 0),
+    # more key blocks than the kernels keep at a time, last tiles of a pair without a row
+    ([1300, 1400, 1537], (2, 1), (64, 128), 0, 0),
+    ([1290, 1281], (2, 2), (128, 128), 130, 300),
+    ([1665], (3, 1), (64, 64), 140, 700),
+    ([1500], (1, 1), (128, 64), 500, 1),
 ]
 
 
@@ -499,6 +504,9 @@ LINEAR = [
     ([257], (2, 4), (128, 128), 0.02, True),
     ([90, 128], (2, 2), (128, 192), 30.0, True),             # decays that leave almost nothing
     ([2, 2, 0, 1, 1], (3, 3), (64, 64), 1.0, False),
+    ([700, 129, 640], (1, 2), (64, 128), 0.01, True),        # several chunks of every kernel
+    ([515], (1, 1), (64, 64), 0.2, True),
+    ([450], (1, 1), (128, 64), 0.05, False),
 ]
 
 
