@@ -3,11 +3,12 @@
 // sequence's first row ("Jamba: Hybrid SSM-Transformer", section 1; "Hymba Guide",
 // Learnable Meta-Tokens; 51cto Hymba-1.5B article, section 2).
 //
-// One 256-thread block per (64 query rows of a sequence, head), the heaviest rows of a
-// sequence first. Key tiles of 64: S (64 x 64) as 4 x 4 per thread from transposed Q and K
-// tiles, one running max and sum per row, P transposed through shared memory, O as 4 rows
-// x DV/16 columns per thread. Bound by the FMA pipe: 2 (dh + dv) flops per visible pair,
-// and the diagonal tiles' masked half on top.
+// One 256-thread block per (tile of 64, 32 or 16 query rows of a sequence, head), the heaviest
+// rows of a sequence first. Key tiles of 64: S as rows / 16 x 4 per thread from transposed Q
+// and K tiles, one running max and sum per row, P transposed through shared memory, O as
+// rows / 16 x DV / 16 per thread, all on packed pairs (two FMAs per instruction). Bound by the FMA
+// pipe for long prompts (2 (dh + dv) flops per visible pair, and the diagonal tiles' masked
+// half on top), by the chain of key tiles for short ones.
 #include "kernels.h"
 #include "ragged.cuh"
 
@@ -15,18 +16,32 @@ namespace hymba {
 
 namespace {
 
-constexpr int QT = 64, KT = 64, LD = QT + 4, NT = 256;
+constexpr int KT = 64, NT = 256;
 
-template <int DH, int DV>
+template <int DH, int DV, int QT>
 struct PackedSimtSmem {
-    alignas(16) float q[DH][LD];  // transposed: [dim][row]
-    alignas(16) float k[DH][LD];  // transposed: [dim][key]
+    alignas(16) float q[DH][QT + 4];  // transposed: [dim][row]
+    alignas(16) float k[DH][KT + 4];  // transposed: [dim][key]
     alignas(16) float v[KT][DV];
-    alignas(16) float p[KT][LD];  // transposed: [key][row]
+    alignas(16) float p[KT][QT + 4];  // transposed: [key][row]
     ragged::FindSmem find;
 };
 
-template <typename T, int DH, int DV>
+// RT consecutive values of a transposed tile (one load)
+template <int RT>
+__device__ __forceinline__ void row_values(const float* p, float (&v)[RT]) {
+    if constexpr (RT == 4) {
+        const float4 a = *reinterpret_cast<const float4*>(p);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    } else if constexpr (RT == 2) {
+        const float2 a = *reinterpret_cast<const float2*>(p);
+        v[0] = a.x; v[1] = a.y;
+    } else {
+        v[0] = *p;
+    }
+}
+
+template <typename T, int DH, int DV, int QT>
 __global__ void __launch_bounds__(NT)
 attn_packed_simt_kernel(const T* __restrict__ q, long long ldq, const T* __restrict__ k, long long ldk,
                         const T* __restrict__ v, long long ldv, const int* __restrict__ cu, int n_seqs, int total,
@@ -34,7 +49,8 @@ attn_packed_simt_kernel(const T* __restrict__ q, long long ldq, const T* __restr
                         int* status) {
     griddep_sync();
     extern __shared__ __align__(16) uint8_t packed_simt_raw[];
-    PackedSimtSmem<DH, DV>& sm = *reinterpret_cast<PackedSimtSmem<DH, DV>*>(packed_simt_raw);
+    PackedSimtSmem<DH, DV, QT>& sm = *reinterpret_cast<PackedSimtSmem<DH, DV, QT>*>(packed_simt_raw);
+    constexpr int RT = QT / 16;  // rows per thread
     const int h = blockIdx.x % H, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const ragged::Item it = ragged::find_item<NT>(sm.find, cu, n_seqs, total, QT, false, blockIdx.x / H, status);
     if (it.seq < 0) return;
@@ -53,13 +69,14 @@ attn_packed_simt_kernel(const T* __restrict__ q, long long ldq, const T* __restr
 #pragma unroll
         for (int e = 0; e < 8; ++e) sm.q[8 * c + e][r] = x[e] * scale_log2;
     }
-    float acc[4][DV / 16], mrun[4], l[4];
+    float2 acc[RT][DV / 32];
+    float mrun[RT], l[RT];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < RT; ++r) {
         mrun[r] = -INFINITY;
         l[r] = 0.f;
 #pragma unroll
-        for (int c = 0; c < DV / 16; ++c) acc[r][c] = 0.f;
+        for (int c = 0; c < DV / 32; ++c) acc[r][c] = make_float2(0.f, 0.f);
     }
     const int i_last = min(i0 + QT, L) - 1;
     const int lo = window > 0 ? max(n_meta, i0 - window + 1) : n_meta;
@@ -85,20 +102,32 @@ attn_packed_simt_kernel(const T* __restrict__ q, long long ldq, const T* __restr
                 *reinterpret_cast<float4*>(&sm.v[r][8 * c + 4]) = make_float4(x[4], x[5], x[6], x[7]);
             }
             odd = __syncthreads_or(odd);
-            float s[4][4] = {};
+            float2 s2[RT][2];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) s2[r][0] = s2[r][1] = make_float2(0.f, 0.f);
 #pragma unroll 8
             for (int d = 0; d < DH; ++d) {
-                const float4 a = *reinterpret_cast<const float4*>(&sm.q[d][4 * ty]);
+                float av[RT];
+                row_values<RT>(&sm.q[d][RT * ty], av);
                 const float4 b = *reinterpret_cast<const float4*>(&sm.k[d][4 * tx]);
-                const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
+                for (int r = 0; r < RT; ++r) {
+                    const float2 a2 = make_float2(av[r], av[r]);
+                    s2[r][0] = __ffma2_rn(a2, make_float2(b.x, b.y), s2[r][0]);
+                    s2[r][1] = __ffma2_rn(a2, make_float2(b.z, b.w), s2[r][1]);
+                }
+            }
+            float s[RT][4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[r][c] = fmaf(av[r], bv[c], s[r][c]);
+            for (int r = 0; r < RT; ++r) {
+                s[r][0] = s2[r][0].x;
+                s[r][1] = s2[r][0].y;
+                s[r][2] = s2[r][1].x;
+                s[r][3] = s2[r][1].y;
             }
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = i0 + 4 * ty + r;
+            for (int r = 0; r < RT; ++r) {
+                const int i = i0 + RT * ty + r;
                 float mx = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -120,41 +149,41 @@ attn_packed_simt_kernel(const T* __restrict__ q, long long ldq, const T* __restr
                 }
                 l[r] = l[r] * f + sum;  // this thread's columns; the 16 threads of the row are added at the end
 #pragma unroll
-                for (int c = 0; c < DV / 16; ++c) acc[r][c] *= f;
+                for (int c = 0; c < DV / 32; ++c) acc[r][c] = __fmul2_rn(acc[r][c], make_float2(f, f));
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                *reinterpret_cast<float4*>(&sm.p[4 * tx + c][4 * ty]) = make_float4(s[0][c], s[1][c], s[2][c], s[3][c]);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) sm.p[4 * tx + c][RT * ty + r] = s[r][c];
             __syncthreads();
             const int nk = min(KT, end - j0);
 #pragma unroll 4
             for (int j = 0; j < nk; ++j) {
-                const float4 a = *reinterpret_cast<const float4*>(&sm.p[j][4 * ty]);
-                const float av[4] = {a.x, a.y, a.z, a.w};
-                bool see[4] = {true, true, true, true};
-                if (odd) {
+                float av[RT];
+                row_values<RT>(&sm.p[j][RT * ty], av);
+                bool see[RT];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int i = i0 + 4 * ty + r, jj = j0 + j;
-                        see[r] = jj <= i && (range == 0 || window <= 0 || i - jj < window);
-                    }
+                for (int r = 0; r < RT; ++r) {
+                    const int i = i0 + RT * ty + r, jj = j0 + j;
+                    see[r] = !odd || (jj <= i && (range == 0 || window <= 0 || i - jj < window));
                 }
 #pragma unroll
                 for (int u = 0; u < DV / 64; ++u) {
                     const float4 b = *reinterpret_cast<const float4*>(&sm.v[j][4 * tx + 64 * u]);
-                    const float bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            acc[r][4 * u + c] = see[r] ? fmaf(av[r], bv[c], acc[r][4 * u + c]) : acc[r][4 * u + c];
+                    for (int r = 0; r < RT; ++r) {
+                        if (!see[r]) continue;
+                        const float2 a2 = make_float2(av[r], av[r]);
+                        acc[r][2 * u] = __ffma2_rn(a2, make_float2(b.x, b.y), acc[r][2 * u]);
+                        acc[r][2 * u + 1] = __ffma2_rn(a2, make_float2(b.z, b.w), acc[r][2 * u + 1]);
+                    }
                 }
             }
         }
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int i = i0 + 4 * ty + r;
+    for (int r = 0; r < RT; ++r) {
+        const int i = i0 + RT * ty + r;
         float sum = l[r];
 #pragma unroll
         for (int w = 1; w < 16; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
@@ -164,16 +193,16 @@ attn_packed_simt_kernel(const T* __restrict__ q, long long ldq, const T* __restr
             T* dst = o + (row0 + i) * ldo + (long long)h * DV + 4 * tx;
 #pragma unroll
             for (int u = 0; u < DV / 64; ++u)
-                ragged::store4(dst + 64 * u, acc[r][4 * u] * inv, acc[r][4 * u + 1] * inv, acc[r][4 * u + 2] * inv,
-                               acc[r][4 * u + 3] * inv);
+                ragged::store4(dst + 64 * u, acc[r][2 * u].x * inv, acc[r][2 * u].y * inv, acc[r][2 * u + 1].x * inv,
+                               acc[r][2 * u + 1].y * inv);
         }
     }
 }
 
-template <typename T, int DH, int DV>
-int launch_dims(const Ctx& ctx, const PackedAttn& a) {
-    auto kern = attn_packed_simt_kernel<T, DH, DV>;
-    const size_t smem = sizeof(PackedSimtSmem<DH, DV>);
+template <typename T, int DH, int DV, int QT>
+int launch_tile(const Ctx& ctx, const PackedAttn& a) {
+    auto kern = attn_packed_simt_kernel<T, DH, DV, QT>;
+    const size_t smem = sizeof(PackedSimtSmem<DH, DV, QT>);
     static std::atomic<unsigned long long> smem_set{0};
     if (!smem_opt_in_once(smem_set, kern, smem, ctx)) return HYMBA_ERR_CUDA;
     const long long blocks = ((long long)ceil_div(a.total, QT) + a.n_seqs) * a.H;
@@ -182,6 +211,18 @@ int launch_dims(const Ctx& ctx, const PackedAttn& a) {
                  static_cast<const T*>(a.k), a.ldk, static_cast<const T*>(a.v), a.ldv, a.cu, a.n_seqs, a.total,
                  static_cast<T*>(a.o), a.ldo, a.H, a.G, a.n_meta, a.window, a.scale * 1.4426950408889634f, ctx.status);
     return HYMBA_OK;
+}
+
+// The smallest tile whose blocks still fit one wave of the 148 SMs (a block's time is a chain of
+// key tiles, shorter with fewer rows), 64 rows where none does. 4 heads of 64 x 128: prompts of
+// 272 and 141 rows 15.8 us in tiles of 16, 19.6 in 32, 31.2 in 64; one of 700 rows 24.0 in 16 (a
+// second wave), 19.8 in 32, 31.2 in 64.
+template <typename T, int DH, int DV>
+int launch_dims(const Ctx& ctx, const PackedAttn& a) {
+    auto blocks = [&](int qt) { return ((long long)ceil_div(a.total, qt) + a.n_seqs) * a.H; };
+    if (blocks(16) <= 148) return launch_tile<T, DH, DV, 16>(ctx, a);
+    if (blocks(32) <= 148) return launch_tile<T, DH, DV, 32>(ctx, a);
+    return launch_tile<T, DH, DV, 64>(ctx, a);
 }
 
 }  // namespace

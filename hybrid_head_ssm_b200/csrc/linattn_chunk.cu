@@ -206,7 +206,8 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
     extern __shared__ __align__(128) uint8_t chunk_raw[];
     ChunkSmem<DK>& sm = *reinterpret_cast<ChunkSmem<DK>*>(chunk_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lg = lane >> 2, lq = lane & 3;
-    const int h = blockIdx.y, s = blockIdx.z, hk = h / (H / Hk), c0 = blockIdx.x * CV;
+    const int h = blockIdx.y, hk = h / (H / Hk), c0 = blockIdx.x * CV;
+    const int s = ragged::longest_first(cu, gridDim.z, total, blockIdx.z);
     int start, len;
     if (!ragged::sequence(cu, s, total, &start, &len)) {
         if (tid == 0) set_status(status, HYMBA_ERR_DEVICE_RANGE);

@@ -29,7 +29,8 @@ linattn_recurrent_kernel(const T* __restrict__ q, long long ldq, const T* __rest
     constexpr int NC = DK / 4 / LPR;            // float4s per lane and row
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane % LPR, rsub = lane / LPR;
-    const int h = blockIdx.y, s = blockIdx.z, hk = h / (H / Hk);
+    const int h = blockIdx.y, hk = h / (H / Hk);
+    const int s = cu ? ragged::longest_first(cu, gridDim.z, total, blockIdx.z) : blockIdx.z;
     const int r0 = (blockIdx.x * (NT / 32) + warp) * VR;  // the warp's first v row
     if (r0 >= dv) return;
     int start = s, len = 1;

@@ -274,7 +274,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     // the state's product reads both operands across their rows (A's bit is 15)
     constexpr uint32_t ID_D = tc::idesc_f16(!F16, 128, DK, true) | (1u << 15);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int c0 = blockIdx.x * DV, h = blockIdx.y, sq = blockIdx.z, hk = h / (a.H / a.Hk);
+    const int c0 = blockIdx.x * DV, h = blockIdx.y, hk = h / (a.H / a.Hk);
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -305,6 +305,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     // setup above touches no global memory; everything below may read the previous
     // kernel's output
     griddep_sync();
+    const int sq = ragged::longest_first(a.cu, gridDim.z, a.total, blockIdx.z);
     int start, len;
     if (!ragged::sequence(a.cu, sq, a.total, &start, &len)) {
         if (tid == 0) set_status(status, HYMBA_ERR_DEVICE_RANGE);

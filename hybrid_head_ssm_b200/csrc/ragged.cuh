@@ -22,6 +22,23 @@ __device__ __forceinline__ bool sequence(const int* cu, int s, int total, int* s
     return a >= 0 && b >= a && b <= total;
 }
 
+// The z-th longest of up to 32 sequences (z itself when there are more): blocks that walk one
+// sequence each start with the longest, so that the last ones to start are short. Every lane of
+// the warp returns it; one round trip to memory.
+__device__ __forceinline__ int longest_first(const int* cu, int n_seqs, int total, int z) {
+    if (n_seqs > 32) return z;
+    const int lane = threadIdx.x & 31;
+    int a = 0, n = -1;
+    if (lane < n_seqs && !sequence(cu, lane, total, &a, &n)) n = 0;
+    int rank = 0;
+    for (int j = 0; j < n_seqs; ++j) {
+        const int m = __shfl_sync(0xffffffffu, n, j);
+        rank += m > n || (m == n && j < lane);
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, lane < n_seqs && rank == z);
+    return __ffs(hit) - 1;
+}
+
 struct FindSmem {
     long long warp_sum[32];
     Item item;
