@@ -240,7 +240,7 @@ __device__ __forceinline__ void scaled_keys(uint8_t (*ks)[TILE], const uint8_t* 
                 part[p][x] = pack2<T>(y.x, y.y);
                 if (p + 1 < PARTS) {
                     const float2 z = unpack2<T>(part[p][x]);
-                    y = __fadd2_rn(y, make_float2(-z.x, -z.y));
+                    y = __ffma2_rn(z, make_float2(-1.f, -1.f), y);  // exact
                 }
             }
         }
@@ -506,17 +506,23 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     }
                 } else {
                     const float base = ai + tab.between[blk][u];
+                    const float2 base2 = make_float2(base, base);
                     const int last = u < blk ? 31 : lane;
+                    if (!plain) {
+                        // a decay of 0 drops what it multiplies, also what is not finite
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[j] = fast_exp2(base + tab.b[32 * u + j]) == 0.f ? 0.f : x[j];
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
                         const float4 bj = *reinterpret_cast<const float4*>(&tab.b[32 * u + j]);
-                        const float d[4] = {bj.x, bj.y, bj.z, bj.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            // (a decay of 0 drops what it multiplies, also what is not finite)
-                            const float w = fast_exp2(base + d[e]);
-                            x[j + e] = j + e <= last && w != 0.f ? w * x[j + e] : 0.f;
-                        }
+                        const float2 d = __fadd2_rn(base2, make_float2(bj.x, bj.y)), e = __fadd2_rn(base2, make_float2(bj.z, bj.w));
+                        const float2 y = __fmul2_rn(make_float2(fast_exp2(d.x), fast_exp2(d.y)), make_float2(x[j], x[j + 1]));
+                        const float2 z = __fmul2_rn(make_float2(fast_exp2(e.x), fast_exp2(e.y)), make_float2(x[j + 2], x[j + 3]));
+                        x[j] = j <= last ? y.x : 0.f;
+                        x[j + 1] = j + 1 <= last ? y.y : 0.f;
+                        x[j + 2] = j + 2 <= last ? z.x : 0.f;
+                        x[j + 3] = j + 3 <= last ? z.y : 0.f;
                     }
                 }
             };
@@ -656,8 +662,17 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         *reinterpret_cast<uint4*>(row + ((((u + e) >> 3) ^ (r & 7)) * 16)) =
                             make_uint4(pack2<T>(y[e] * fs, y[e + 1] * fs), pack2<T>(y[e + 2] * fs, y[e + 3] * fs),
                                        pack2<T>(y[e + 4] * fs, y[e + 5] * fs), pack2<T>(y[e + 6] * fs, y[e + 7] * fs));
+                    const float2 d2 = make_float2(dec, dec);
+                    if (dec0 == 0.f) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) y[e] = dec0 == 0.f ? 0.f : y[e] * dec;
+                        for (int e = 0; e < 32; ++e) y[e] = 0.f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 z = __fmul2_rn(make_float2(y[e], y[e + 1]), d2);
+                        y[e] = z.x;
+                        y[e + 1] = z.y;
+                    }
                     tc::tmem_st32(dc + u, *reinterpret_cast<uint32_t(*)[32]>(&y));
                 }
                 tc::tmem_wait_st();
