@@ -165,6 +165,7 @@ struct LinAttn {
     long long ldq, ldk, ldv, ldo, ldg;
     const float *g, *state_in;
     float* state_out;
+    void* ws;
     const int* cu;
     int n_seqs, total, Hk, H, dk, dv;
     float scale;
@@ -175,7 +176,9 @@ int launch_linattn_recurrent(const Ctx& ctx, const LinAttn& a);
 template <typename T>
 int launch_linattn_chunk(const Ctx& ctx, const LinAttn& a);
 // The same in chunks of 128 rows on the tcgen05 tensor cores, for key dim 64.
-bool linattn_tc_applies(const LinAttn& a);
+// Few long sequences are cut into segments, whose states meet in ws (linattn_tc_bytes).
+bool linattn_tc_applies(int dk, int total);
+size_t linattn_tc_bytes(int n_seqs, int total, int H, int dv);
 template <typename T>
 int launch_linattn_tc(const Ctx& ctx, const LinAttn& a);
 

@@ -30,9 +30,14 @@
 // to the rows' type, like any MMA operand. fp16 has little range: P's rows, the copy's rows and
 // K' are brought to the middle of it by powers of two that the fp32 values give back (the
 // state in TMEM carries K's power, changed together with its decay).
-// A CTA that noted a value of V that is not finite computes its sequence once more by the
+// Few long sequences are cut into segments of whole chunks (`segment_rows`): the same kernel first
+// forms what each segment adds to a state of zero, a small one turns these into the state before
+// each segment, and the segments then run side by side.
+// A CTA that noted a value of V that is not finite computes its rows once more by the
 // recurrence, in which nothing reaches a row that does not see it.
 // Bound: HBM (q, k, v read and o written once per 128 value columns).
+#include <algorithm>
+
 #include "attn_tile.cuh"
 #include "kernels.h"
 #include "ragged.cuh"
@@ -91,8 +96,13 @@ struct Args {
     const float *g, *state_in;
     float* state_out;
     const int* cu;
-    int total, Hk, H, dv;
+    int n_seqs, total, Hk, H, dv;
     float log2_scale;
+    // sequences in segments of `seg` rows (0: whole): item t of all sequences' `items` segments starts
+    // from starts[t] [H, dv, DK], if the sequence has more than one; decays [items, H] are the
+    // segments' log2 decays
+    int seg, items;
+    float *starts, *decays;
 };
 
 __device__ __forceinline__ void fail(volatile int* abort, int* status, int role, int step, int bar) {
@@ -122,6 +132,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
 // are real.
 struct LaneTables {
     float a[4], b[4], e[4], w[4], B[3][4], between, dec;
+    double total;  // the chunk's log2 decay
     int resets, grows;
     __device__ __forceinline__ void make(const float (&g)[4], int n, float lsc) {
         constexpr double LOG2E = 1.4426950408889634;
@@ -169,6 +180,7 @@ struct LaneTables {
         grows = __any_sync(0xffffffffu, up);
 #pragma unroll
         for (int o = 16; o; o >>= 1) down += __shfl_xor_sync(0xffffffffu, down, o);
+        total = last;
         dec = fast_exp2((float)last);
         resets = !(down * 1.4426950f + fminf(lsc, 0.f) > -120.f);
     }
@@ -191,20 +203,21 @@ struct LaneTables {
     }
 };
 
-// One value column of a sequence by the recurrence.
+// One value column of `len` rows by the recurrence, from the state row `from` (NULL: zero) to
+// `to` (NULL: not kept); o only where asked for.
 template <typename T>
-__device__ __noinline__ void recurrence(const Args& a, int s, int h, int start, int len, int col) {
+__device__ __noinline__ void recurrence(const Args& a, const float* from, float* to, bool with_o, int h, int start, int len,
+                                        int col) {
     const int hk = h / (a.H / a.Hk);
     const T* q = static_cast<const T*>(a.q) + start * a.ldq + (long long)hk * DK;
     const T* k = static_cast<const T*>(a.k) + start * a.ldk + (long long)hk * DK;
     const T* v = static_cast<const T*>(a.v) + start * a.ldv + (long long)h * a.dv + col;
     T* o = static_cast<T*>(a.o) + start * a.ldo + (long long)h * a.dv + col;
     const float* g = a.g + start * a.ldg + h;
-    const long long at = (((long long)s * a.H + h) * a.dv + col) * DK;
     const float scale = exp2f(a.log2_scale);
     float S[DK];
 #pragma unroll
-    for (int e = 0; e < DK; ++e) S[e] = a.state_in ? a.state_in[at + e] : 0.f;
+    for (int e = 0; e < DK; ++e) S[e] = from ? from[e] : 0.f;
 #pragma unroll 1
     for (int t = 0; t < len; ++t) {
         const float dec = expf(g[t * a.ldg]), x = to_f(v[t * a.ldv]);
@@ -214,11 +227,11 @@ __device__ __noinline__ void recurrence(const Args& a, int s, int h, int start, 
             S[e] = fmaf(x, to_f(k[t * a.ldk + e]), fade(dec, S[e]));
             sum = fmaf(S[e], to_f(q[t * a.ldq + e]), sum);
         }
-        o[t * a.ldo] = from_f<T>(sum * scale);
+        if (with_o) o[t * a.ldo] = from_f<T>(sum * scale);
     }
-    if (a.state_out)
+    if (to)
 #pragma unroll
-        for (int e = 0; e < DK; ++e) a.state_out[at + e] = S[e];
+        for (int e = 0; e < DK; ++e) to[e] = S[e];
 }
 
 // Row r of K' = w k as parts of T; w = 0 drops the row. The 16-byte pieces are swizzled by the row.
@@ -260,7 +273,8 @@ __device__ __forceinline__ void ld32(uint32_t addr, float (&x)[32]) {
     tc::tmem_ld32(addr, *reinterpret_cast<uint32_t(*)[32]>(&x));
 }
 
-template <typename T, int DV>
+// STATE: only the state that a segment adds to nothing, and its decay, for the next segment's start.
+template <typename T, int DV, bool STATE>
 __global__ void __launch_bounds__(NT, 1)
 linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const Args a, int* status) {
@@ -284,7 +298,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         }
         for (int i = 0; i < NTAB; ++i) {
             tc::mbar_init(&s.tab_full[i], 32);
-            tc::mbar_init(&s.tab_empty[i], 12);
+            tc::mbar_init(&s.tab_empty[i], STATE ? 4 : 12);
         }
         tc::mbar_init(&s.s1_full, 1);
         tc::mbar_init(&s.p_full, 128);
@@ -305,16 +319,39 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     // setup above touches no global memory; everything below may read the previous
     // kernel's output
     griddep_sync();
-    const int sq = ragged::longest_first(a.cu, gridDim.z, a.total, blockIdx.z);
-    int start, len;
-    if (!ragged::sequence(a.cu, sq, a.total, &start, &len)) {
-        if (tid == 0) set_status(status, HYMBA_ERR_DEVICE_RANGE);
-        return;
+    int start, len, item = 0;
+    const float* from;  // the state before the first row and after the last, of these columns
+    float* to;
+    const long long per = (long long)a.dv * DK;
+    if (a.seg == 0) {
+        const int sq = ragged::longest_first(a.cu, gridDim.z, a.total, blockIdx.z);
+        if (!ragged::sequence(a.cu, sq, a.total, &start, &len)) {
+            if (tid == 0) set_status(status, HYMBA_ERR_DEVICE_RANGE);
+            return;
+        }
+        from = a.state_in ? a.state_in + ((long long)sq * a.H + h) * per + c0 * DK : nullptr;
+        to = a.state_out ? a.state_out + ((long long)sq * a.H + h) * per + c0 * DK : nullptr;
+    } else {
+        item = blockIdx.z;
+        const ragged::Item it = ragged::find_item32(a.cu, a.n_seqs, a.total, a.seg, true, item, item == 0, status);
+        if (it.seq < 0) return;
+        start = it.start + it.tile * a.seg;
+        len = min(a.seg, it.len - it.tile * a.seg);
+        const bool last = (it.tile + 1) * a.seg >= it.len;
+        if (STATE && last) return;
+        const long long at = ((long long)it.seq * a.H + h) * per + c0 * DK;
+        // (state_out may be state_in: of a sequence that was cut only `starts` is read)
+        from = it.len > a.seg ? a.starts + ((long long)item * a.H + h) * per + c0 * DK : a.state_in ? a.state_in + at : nullptr;
+        to = last && a.state_out ? a.state_out + at : nullptr;
+        if (STATE) {
+            if (item + 1 >= a.items) return;  // (offsets out of order)
+            from = nullptr;
+            to = a.starts + ((long long)(item + 1) * a.H + h) * per + c0 * DK;
+        }
     }
-    const long long state_at = (((long long)sq * a.H + h) * a.dv + c0) * DK;
     if (len == 0) {
-        if (a.state_out)
-            for (int i = tid; i < DV * DK; i += NT) a.state_out[state_at + i] = a.state_in ? a.state_in[state_at + i] : 0.f;
+        if (to)
+            for (int i = tid; i < DV * DK; i += NT) to[i] = from ? from[i] : 0.f;
         return;
     }
     if (warp == 1) {
@@ -338,8 +375,8 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 const int b = c & 1;
                 // the stage's chunk is done with its last product, which follows every read of it
                 if (!tc::mbar_wait(&s.empty[b], ((c >> 1) & 1) ^ 1, abort, wlim)) { fail(abort, status, 0, c, 1); break; }
-                tc::mbar_arrive_expect_tx(&s.full[b], (2 + DV / 64) * TILE);
-                tc::tma_load_2d(s.q[b], &tmQ, &s.full[b], hk * DK, start + c * CQ);
+                tc::mbar_arrive_expect_tx(&s.full[b], (STATE ? 1 + DV / 64 : 2 + DV / 64) * TILE);
+                if (!STATE) tc::tma_load_2d(s.q[b], &tmQ, &s.full[b], hk * DK, start + c * CQ);
                 tc::tma_load_2d(s.k[b], &tmK, &s.full[b], hk * DK, start + c * CQ);
 #pragma unroll
                 for (int p = 0; p < DV / 64; ++p)
@@ -364,13 +401,16 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 const uint32_t ph2 = (c >> 1) & 1, ph = c & 1;
                 const uint32_t qa = tc::smem_u32(s.q[b]), ka = tc::smem_u32(s.k[b]), va = tc::smem_u32(s.v[b][0]);
                 wait(&s.full[b], ph2, c, 1);
-                if (c > 0) wait(&s.o_full, ph ^ 1, c, 2);  // S1 overwrites P
-                if (!ok) break;
-                tc::tc_fence_after();
+                if (!STATE) {
+                    if (c > 0) wait(&s.o_full, ph ^ 1, c, 2);  // S1 overwrites P
+                    if (!ok) break;
+                    tc::tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk)
-                    tc::mma_f16_ss(tmem + TM_S1, tc::sdesc_k_sw128(qa + kk * 32), tc::sdesc_k_sw128(ka + kk * 32), ID_S1, kk > 0);
-                tc::mma_commit(&s.s1_full);
+                    for (int kk = 0; kk < DK / 16; ++kk)
+                        tc::mma_f16_ss(tmem + TM_S1, tc::sdesc_k_sw128(qa + kk * 32), tc::sdesc_k_sw128(ka + kk * 32), ID_S1,
+                                       kk > 0);
+                    tc::mma_commit(&s.s1_full);
+                }
                 // the state, once it is decayed and K' is there
                 wait(&s.s_ready, ph, c, 3);
                 wait(&s.v_ok[b], ph2, c, 4);
@@ -386,6 +426,10 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                                        tc::sdesc_mn_sw128(ks + kk * 2048, TILE), ID_D, 1);
                 }
                 tc::mma_commit(&s.d_done);
+                if (STATE) {
+                    tc::mma_commit(&s.empty[b]);
+                    continue;
+                }
                 if (c > 0) wait(&s.o_free, ph ^ 1, c, 6);  // O and O2 of the chunk before are read
                 if (!ok) break;
                 tc::tc_fence_after();
@@ -418,6 +462,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             }
         };
         fetch(0);
+        double total = 0.0;
         for (int c = 0; c < nc; ++c) {
             LaneTables t;
             t.make(x, len - c * CQ, a.log2_scale);
@@ -428,7 +473,9 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             }
             t.store(s.tab[c % NTAB]);
             tc::mbar_arrive(&s.tab_full[c % NTAB]);
+            total += t.total;
         }
+        if (STATE && blockIdx.x == 0 && lane == 0) a.decays[(long long)item * a.H + h] = (float)total;
     } else if (warp == 3) {
         // ---------------- V ----------------
         for (int c = 0; c < nc; ++c) {
@@ -469,6 +516,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             tc::mbar_arrive(&s.v_ok[b]);
         }
     } else if (warp < 8) {
+        if constexpr (!STATE) {
         // ---------------- P: row i of the chunk, TMEM lane i ----------------
         const int blk = warp & 3, i = blk * 32 + lane;
         const uint32_t lane_base = (uint32_t)(blk * 32) << 16;
@@ -569,6 +617,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&s.tab_empty[c % NTAB]);
         }
+        }
     } else if (warp < 12) {
         // ---------------- the state (row r a value), then K' (row r of the chunk) ----------------
         const int quad = warp & 3, r = quad * 32 + lane;
@@ -589,7 +638,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
                     float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (a.state_in) z = *reinterpret_cast<const float4*>(a.state_in + state_at + (long long)r * DK + u + e);
+                    if (from) z = *reinterpret_cast<const float4*>(from + (long long)r * DK + u + e);
                     y[e] = z.x;
                     y[e + 1] = z.y;
                     y[e + 2] = z.z;
@@ -637,7 +686,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             tc::tc_fence_after();
             if (mine) {
                 float fs = 1.f, dec = dec0;
-                if (F16) {
+                if (F16 && !STATE) {
                     float m = 0.f;
 #pragma unroll 1
                     for (int u = 0; u < DK; u += 32) {
@@ -649,6 +698,8 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     }
                     fs = to_middle(m, -100, 100);
                     s.col[c % 3][r] = inverse(fs) * inverse(power);
+                }
+                if (F16) {
                     dec = dec0 * (fk * inverse(power));
                 }
                 uint8_t* row = s.s16[b] + r * 128;
@@ -658,7 +709,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     ld32(dc + u, y);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
+                    for (int e = 0; !STATE && e < 32; e += 8)
                         *reinterpret_cast<uint4*>(row + ((((u + e) >> 3) ^ (r & 7)) * 16)) =
                             make_uint4(pack2<T>(y[e] * fs, y[e + 1] * fs), pack2<T>(y[e + 2] * fs, y[e + 3] * fs),
                                        pack2<T>(y[e + 4] * fs, y[e + 5] * fs), pack2<T>(y[e + 6] * fs, y[e + 7] * fs));
@@ -686,10 +737,10 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             tc::mbar_arrive(&s.k_ready);
         }
         wait(&s.d_done, (nc - 1) & 1, nc, 33);
-        if (ok && mine && a.state_out && !*reinterpret_cast<volatile int*>(&s.dirty)) {
+        if (ok && mine && to && !*reinterpret_cast<volatile int*>(&s.dirty)) {
             tc::tc_fence_after();
             const float back = F16 ? inverse(power) : 1.f;
-            float* to = a.state_out + state_at + (long long)r * DK;
+            float* row = to + (long long)r * DK;
 #pragma unroll 1
             for (int u = 0; u < DK; u += 32) {
                 float y[32];
@@ -697,11 +748,11 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 tc::tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<float4*>(to + u + e) =
+                    *reinterpret_cast<float4*>(row + u + e) =
                         make_float4(y[e] * back, y[e + 1] * back, y[e + 2] * back, y[e + 3] * back);
             }
         }
-    } else {
+    } else if constexpr (!STATE) {
         // ---------------- o: row r of the chunk ----------------
         const int quad = warp & 3, r = quad * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
@@ -786,7 +837,64 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
     }
-    if (s.dirty && !s.abort && tid >= 128 && tid < 128 + DV) recurrence<T>(a, sq, h, start, len, c0 + tid - 128);
+    if (s.dirty && !s.abort && tid >= 128 && tid < 128 + DV) {
+        const long long row = (long long)(tid - 128) * DK;
+        recurrence<T>(a, from ? from + row : nullptr, to ? to + row : nullptr, !STATE, h, start, len, c0 + tid - 128);
+    }
+}
+
+// The state before every segment of a sequence that was cut: the state before the segment before,
+// decayed, plus what that segment added (already in `starts`), one after the other. The decay in
+// two halves: over a whole segment it may leave fp32's range where the product does not; below
+// 2^-159 it drops what it multiplies, like one row's.
+__global__ void __launch_bounds__(256) linattn_starts_kernel(const Args a) {
+    griddep_sync();
+    const int h = blockIdx.y, sq = blockIdx.z;
+    const long long per = (long long)a.dv * DK, at = (long long)blockIdx.x * 1024 + threadIdx.x * 4;
+    int start, len;
+    if (at >= per || !ragged::sequence(a.cu, sq, a.total, &start, &len) || len <= a.seg) return;
+    int first = 0;  // the sequence's first item
+    for (int j = 0; j < sq; ++j) {
+        int x, n;
+        if (ragged::sequence(a.cu, j, a.total, &x, &n)) first += n ? (n + a.seg - 1) / a.seg : 1;
+    }
+    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.state_in) S = *reinterpret_cast<const float4*>(a.state_in + ((long long)sq * a.H + h) * per + at);
+    const int end = min(first + (len + a.seg - 1) / a.seg, a.items);  // (more only with offsets out of order)
+    for (int i = first; i < end; ++i) {
+        if (i > first) {
+            const float d2 = a.decays[(long long)(i - 1) * a.H + h], d = exp2f(0.5f * d2);
+            const float4 u = *reinterpret_cast<const float4*>(a.starts + ((long long)i * a.H + h) * per + at);
+            auto next = [&](float x, float add) { return (d2 < -159.f ? 0.f : x * d * d) + add; };
+            S = make_float4(next(S.x, u.x), next(S.y, u.y), next(S.z, u.z), next(S.w, u.w));
+        }
+        *reinterpret_cast<float4*>(a.starts + ((long long)i * a.H + h) * per + at) = S;
+    }
+}
+
+// How sequences are cut where they and their heads leave SMs idle: 0 (whole), or rows per segment
+// such that the segments' blocks fill the GPU once. Two more launches and a second look at k and v
+// ask for at least three segments, of at least three chunks. bf16, heads of 64 x 128, cut and
+// whole: one prompt of 8192 rows and 25 heads 90 and 194 us, of 2000 rows 37 and 52 us; of 30,000
+// rows and 8 heads 103 and 678 us; three of 3000, 2500 and 10 rows and 8 heads 36 and 76 us.
+int segment_rows(int n_seqs, int total, int H, int dv) {
+    const long long per = (long long)H * (dv % 128 ? dv / 64 : dv / 128);  // blocks of a segment
+    const long long want = 148 / per - (n_seqs - 1);  // segments of n sequences: up to n - 1 more than of one
+    if (n_seqs > 32 || want < 3) return 0;
+    const long long rows = std::max<long long>(3 * CQ, round_up((total + want - 1) / want, CQ));
+    return total <= 2 * rows || total < 9 * CQ ? 0 : (int)rows;
+}
+long long segment_items(int seg, int n_seqs, int total) { return (total + seg - 1) / seg + n_seqs - 1; }
+
+template <typename T, int DV, bool STATE>
+int launch_pass(const Ctx& ctx, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Args& a, int z) {
+    auto kern = linattn_tc_kernel<T, DV, STATE>;
+    const size_t smem = sizeof(TcSmem<std::is_same<T, bf16>::value ? 3 : 2>) + 1024;
+    static std::atomic<unsigned long long> smem_set{0};
+    if (!smem_opt_in_once(smem_set, kern, smem, ctx)) return HYMBA_ERR_CUDA;
+    HYMBA_LAUNCH(ctx, STATE ? "linattn_segment_states" : "linattn_chunk", kern, dim3(a.dv / DV, a.H, z), NT, smem, tq, tk, tv, a,
+                 ctx.status);
+    return HYMBA_OK;
 }
 
 template <typename T, int DV>
@@ -797,31 +905,51 @@ int launch_dv(const Ctx& ctx, const LinAttn& x) {
         !tc::make_tmap_2d(&tk, x.k, BF16, x.total, (uint64_t)x.Hk * DK, x.ldk, CQ) ||
         !tc::make_tmap_2d(&tv, x.v, BF16, x.total, (uint64_t)x.H * x.dv, x.ldv, CQ))
         return HYMBA_ERR_UNSUPPORTED;
-    auto kern = linattn_tc_kernel<T, DV>;
-    const size_t smem = sizeof(TcSmem<BF16 ? 3 : 2>) + 1024;
-    static std::atomic<unsigned long long> smem_set{0};
-    if (!smem_opt_in_once(smem_set, kern, smem, ctx)) return HYMBA_ERR_CUDA;
+    Args a;
+    a.q = x.q; a.k = x.k; a.v = x.v; a.o = x.o;
+    a.ldq = x.ldq; a.ldk = x.ldk; a.ldv = x.ldv; a.ldo = x.ldo; a.ldg = x.ldg;
+    a.g = x.g;
+    a.state_in = x.state_in;
+    a.state_out = x.state_out;
+    a.cu = x.cu;
+    a.n_seqs = x.n_seqs; a.total = x.total; a.Hk = x.Hk; a.H = x.H; a.dv = x.dv;
+    a.log2_scale = log2f(x.scale);
+    a.seg = segment_rows(x.n_seqs, x.total, x.H, x.dv);
+    a.items = 0;
+    a.starts = a.decays = nullptr;
+    if (a.seg) {
+        const int items = a.items = (int)segment_items(a.seg, x.n_seqs, x.total);
+        a.decays = static_cast<float*>(x.ws);
+        a.starts = a.decays + round_up((long long)items * x.H, 64);
+        int rc = launch_pass<T, DV, true>(ctx, tq, tk, tv, a, items);
+        if (rc) return rc;
+        HYMBA_LAUNCH(ctx, "linattn_starts", linattn_starts_kernel, dim3(ceil_div((long long)x.dv * DK, 1024), x.H, x.n_seqs), 256,
+                     0, a);
+        return launch_pass<T, DV, false>(ctx, tq, tk, tv, a, items);
+    }
     // sequences on the grid's slowest dimension, in runs it can hold
     for (int s0 = 0; s0 < x.n_seqs; s0 += 65535) {
         const int n = x.n_seqs - s0 < 65535 ? x.n_seqs - s0 : 65535;
         const long long st0 = (long long)s0 * x.H * x.dv * DK;
-        Args a;
-        a.q = x.q; a.k = x.k; a.v = x.v; a.o = x.o;
-        a.ldq = x.ldq; a.ldk = x.ldk; a.ldv = x.ldv; a.ldo = x.ldo; a.ldg = x.ldg;
-        a.g = x.g;
         a.state_in = x.state_in ? x.state_in + st0 : nullptr;
         a.state_out = x.state_out ? x.state_out + st0 : nullptr;
         a.cu = x.cu + s0;
-        a.total = x.total; a.Hk = x.Hk; a.H = x.H; a.dv = x.dv;
-        a.log2_scale = log2f(x.scale);
-        HYMBA_LAUNCH(ctx, "linattn_chunk", kern, dim3(x.dv / DV, x.H, n), NT, smem, tq, tk, tv, a, ctx.status);
+        const int rc = launch_pass<T, DV, false>(ctx, tq, tk, tv, a, n);
+        if (rc) return rc;
     }
     return HYMBA_OK;
 }
 
 }  // namespace
 
-bool linattn_tc_applies(const LinAttn& a) { return a.dk == DK && a.total > 0; }
+bool linattn_tc_applies(int dk, int total) { return dk == DK && total > 0; }
+
+size_t linattn_tc_bytes(int n_seqs, int total, int H, int dv) {
+    const int seg = segment_rows(n_seqs, total, H, dv);
+    if (!seg) return 256;
+    const long long items = segment_items(seg, n_seqs, total);
+    return (size_t)(round_up(items * H, 64) + items * H * dv * DK) * 4;
+}
 
 template <typename T>
 int launch_linattn_tc(const Ctx& ctx, const LinAttn& a) {

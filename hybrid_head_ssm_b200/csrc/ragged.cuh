@@ -44,6 +44,36 @@ struct FindSmem {
     Item item;
 };
 
+// find_item for up to 32 sequences: every warp for itself, one round trip, no barrier. `report`:
+// whether this warp records offsets that are out of order.
+__device__ __forceinline__ Item find_item32(const int* cu, int n_seqs, int total, int rows, bool min_one, long long t,
+                                            bool report, int* status) {
+    const int lane = threadIdx.x & 31;
+    int a = 0, n = 0, c = 0;
+    if (lane < n_seqs) {
+        if (sequence(cu, lane, total, &a, &n)) {
+            c = (n + rows - 1) / rows;
+            if (min_one && c == 0) c = 1;
+        } else if (report) {
+            set_status(status, HYMBA_ERR_DEVICE_RANGE);
+        }
+    }
+    long long incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, t >= incl - c && t < incl);
+    const int at = hit ? __ffs(hit) - 1 : 0;
+    Item it;
+    it.seq = hit ? at : -1;
+    it.start = __shfl_sync(0xffffffffu, a, at);
+    it.len = __shfl_sync(0xffffffffu, n, at);
+    it.tile = (int)(t - __shfl_sync(0xffffffffu, incl - c, at));
+    return it;
+}
+
 // The t-th work item when every sequence is cut into ceil(len / rows) runs (min_one: at
 // least one, so that empty sequences are items too). Called by all NT threads of the
 // block; each thread counts a run of consecutive sequences and one block scan finds the
@@ -52,32 +82,7 @@ template <int NT>
 __device__ Item find_item(FindSmem& sm, const int* cu, int n_seqs, int total, int rows, bool min_one, long long t,
                           int* status) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (n_seqs <= 32) {
-        // every warp for itself: one round trip, no barrier
-        int a = 0, n = 0, c = 0;
-        if (lane < n_seqs) {
-            if (sequence(cu, lane, total, &a, &n)) {
-                c = (n + rows - 1) / rows;
-                if (min_one && c == 0) c = 1;
-            } else if (blockIdx.x == 0 && warp == 0) {
-                set_status(status, HYMBA_ERR_DEVICE_RANGE);
-            }
-        }
-        long long incl = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, t >= incl - c && t < incl);
-        const int at = hit ? __ffs(hit) - 1 : 0;
-        Item it;
-        it.seq = hit ? at : -1;
-        it.start = __shfl_sync(0xffffffffu, a, at);
-        it.len = __shfl_sync(0xffffffffu, n, at);
-        it.tile = (int)(t - __shfl_sync(0xffffffffu, incl - c, at));
-        return it;
-    }
+    if (n_seqs <= 32) return find_item32(cu, n_seqs, total, rows, min_one, t, blockIdx.x == 0 && warp == 0, status);
     const int per = (n_seqs + NT - 1) / NT;
     const int s0 = min(tid * per, n_seqs), s1 = min(s0 + per, n_seqs);
     if (tid == 0) sm.item.seq = -1;

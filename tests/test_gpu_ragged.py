@@ -633,6 +633,133 @@ def test_linear_attention_offsets_out_of_order_are_left_out(dt):
         assert end[b].isnan().all(), bad  # not written
 
 
+# few long prompts, whose rows several blocks share
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,heads,dims", [([1409], (1, 1), (64, 64)), ([0, 1300, 1, 900, 384], (2, 4), (64, 128)),
+                                             ([2304, 2305], (3, 3), (64, 192)), ([1152] + [0] * 31, (1, 2), (64, 128))])
+@pytest.mark.parametrize("start", [False, True])
+def test_linear_attention_few_long_prompts(dt, lens, heads, dims, start):
+    torch, hy, rt, code, tdt = _mods()
+    (Hk, H), (dk, dv) = heads, dims
+    x = _linear(dt, lens, Hk, H, dk, dv, 56, gap=8, decay=0.01)
+    q, k, v, g, st, cu = x
+    g[::500] = -400.0  # a segment's whole decay out of fp32's range
+    o, end = _run_linear(dt, x, Hk, H, dk, dv, start, in_place=start)
+    _status_ok(hy, torch)
+    want, oa, we, ea = ro.linear_attention(_np(q), _np(k), _np(v), _np(g), _offsets(lens), Hk, H, dk ** -0.5,
+                                           _np(st) if start else None)
+    n = sum(lens)
+    ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
+    _hold(_np(o)[:n], want[:n], ob[:n], f"{dt} {lens} o", 2 * U[dt] + 2.0 ** -17)
+    _hold(_np(end), we, eb, f"{dt} {lens} state", 2.0 ** -16)
+    assert (o[n:] == 7).all()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_linear_attention_few_long_prompts_non_finite(dt):
+    """A NaN in the second segment of a long prompt, and a reset two segments later: rows before
+    the one and behind the other keep their values."""
+    torch, hy, rt, code, tdt = _mods()
+    lens, Hk, H, dk, dv = [1800, 30], 2, 2, 64, 64
+    x = _linear(dt, lens, Hk, H, dk, dv, 57, decay=0.01)
+    q, k, v, g, st, cu = x
+    n, at, reset = sum(lens), 500, 1300
+    g[reset] = float("-inf")
+    want, oa, we, ea = ro.linear_attention(*(_np(t[:n]) for t in (q, k, v, g)), _offsets(lens), Hk, H, dk ** -0.5, _np(st))
+    ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
+    for what in ("k", "v"):
+        y = [t.clone() for t in (q, k, v)]
+        y["qkv".index(what)][at] = float("nan")
+        o, end = _run_linear(dt, (*y, g, st, cu), Hk, H, dk, dv, True)
+        _status_ok(hy, torch)
+        got = _np(o)[:n]
+        sees = np.zeros(n, dtype=bool)
+        sees[at:reset] = True
+        _hold(got[~sees], want[~sees], ob[~sees], f"{dt} {what}, rows that do not see it")
+        assert np.isnan(got[sees]).all()
+        _hold(_np(end), we, eb, f"{dt} {what} states")
+
+
+def test_linear_attention_few_long_prompts_offsets_out_of_order():
+    """More segments than the offsets may name: nothing outside the buffers is touched."""
+    torch, hy, rt, code, tdt = _mods()
+    Hk, H, dk, dv = 2, 2, 64, 64
+    x = list(_linear("bf16", [1500, 100, 100], Hk, H, dk, dv, 58, pad=0))
+    x[5] = torch.tensor([0, 1700, 0, 1700], dtype=torch.int32, device="cuda")
+    o, end = _run_linear("bf16", x, Hk, H, dk, dv, True)
+    _status_range(hy, torch)
+    assert end[1].isnan().all()  # the one with a negative length, not written
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+def test_linear_attention_many_short_prompts(dt):
+    """More sequences than a warp has lanes, and none with any row at all."""
+    torch, hy, rt, code, tdt = _mods()
+    Hk, H, dk, dv = 2, 2, 64, 64
+    lens = [(7 * i) % 40 for i in range(70)]
+    x = _linear(dt, lens, Hk, H, dk, dv, 59)
+    q, k, v, g, st, cu = x
+    o, end = _run_linear(dt, x, Hk, H, dk, dv, True, in_place=True)
+    _status_ok(hy, torch)
+    want, oa, we, ea = ro.linear_attention(_np(q), _np(k), _np(v), _np(g), _offsets(lens), Hk, H, dk ** -0.5, _np(st))
+    ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
+    n = sum(lens)
+    _hold(_np(o)[:n], want[:n], ob[:n], f"{dt} o", 2 * U[dt] + 2.0 ** -17)
+    _hold(_np(end), we, eb, f"{dt} state", 2.0 ** -16)
+    s = hy.linattn_shape(Hk, H, dk, dv, code[dt])
+    none = lambda t: t[:0]
+    out = torch.full_like(st, float("nan"))
+    rt.linattn_prefill(s, none(q), none(k), none(v), none(g), torch.zeros_like(cu), none(o), rt.linattn_workspace(s, 70, 0),
+                       state_in=st, state_out=out)
+    _status_ok(hy, torch)
+    assert (out == st).all()
+
+
+@pytest.mark.parametrize("lens", [[1500], [300] * 3])
+def test_linear_attention_captured_and_on_two_streams(lens):
+    """Two calls at once, each with its own workspace, and a captured one replayed on new inputs,
+    equal the call alone bit for bit."""
+    torch, hy, rt, code, tdt = _mods()
+    Hk, H, dk, dv = 2, 4, 64, 128
+    s = hy.linattn_shape(Hk, H, dk, dv, code["bf16"])
+    xs = [_linear("bf16", lens, Hk, H, dk, dv, 63 + i, pad=0) for i in range(2)]
+
+    def call(x, ws):
+        q, k, v, g, st, cu = x
+        o, end = torch.zeros_like(v), torch.zeros_like(st)
+        return o, end, lambda: rt.linattn_prefill(s, q, k, v, g, cu, o, ws, state_in=st, state_out=end)
+
+    wss = [rt.linattn_workspace(s, len(lens), sum(lens)) for _ in range(2)]
+    alone = []
+    for x, ws in zip(xs, wss):
+        o, end, f = call(x, ws)
+        f()
+        alone.append((o, end))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    runs = [call(x, ws) for x, ws in zip(xs, wss)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for st, r in zip(streams, runs):
+            with torch.cuda.stream(st):
+                r[2]()
+    torch.cuda.synchronize()
+    for (o, end), r in zip(alone, runs):
+        assert torch.equal(o, r[0]) and torch.equal(end, r[1])
+    buf = tuple(t.clone() for t in xs[0])
+    o, end, f = call(buf, wss[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f()
+    for x, (wo, we) in zip(xs, alone):
+        for to, t in zip(buf, x):
+            to.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, wo) and torch.equal(end, we)
+    _status_ok(hy, torch)
+
+
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("batch,heads,dims", [(1, (4, 4), (64, 128)), (7, (1, 50), (16, 64)), (3, (5, 25), (128, 64)),
                                               (40, (2, 2), (64, 512))])
