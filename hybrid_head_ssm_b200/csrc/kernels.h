@@ -177,7 +177,7 @@ template <typename T>
 int launch_linattn_chunk(const Ctx& ctx, const LinAttn& a);
 // The same in chunks of 128 rows on the tcgen05 tensor cores, for key dim 64.
 // Few long sequences are cut into segments, whose states meet in ws (linattn_tc_bytes).
-bool linattn_tc_applies(int dk, int total);
+bool linattn_tc_applies(int dk);
 size_t linattn_tc_bytes(int n_seqs, int total, int H, int dv);
 template <typename T>
 int launch_linattn_tc(const Ctx& ctx, const LinAttn& a);

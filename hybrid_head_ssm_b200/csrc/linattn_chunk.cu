@@ -1,4 +1,4 @@
-// Linear attention with a decay per head, chunked form on the tensor cores (16-bit rows):
+// Linear attention with a decay per head, chunked form on the warp MMAs (16-bit rows, key dim 16 or 128):
 // S_t = exp(g_t) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t over packed prompts ("Lecture 04 -
 // Beyond the Dense Transformer", section 3: with a scalar decay per head the recurrence is a
 // masked product with a semiseparable matrix and can be computed as blocks of matmuls). Per
@@ -19,16 +19,17 @@
 // the fp32 distances of cs_i and cs_j from the cs at the start of i's 16 rows, so it is right
 // to fp32 after any other row (one that forgets everything included) and never formed from two
 // factors. P and the copy of S that meets q are rounded to the rows' type, like any MMA operand;
-// the scaled v of the state update enters as two 16-bit parts, so the fp32 state keeps 16 bits
-// or more of every term. fp16 has
-// little range: P's rows, S's copy and v are brought to the middle of it by powers of two,
+// the scaled v of the state update enters as three parts (bf16) or two (fp16), so the fp32 state
+// keeps 22 bits or more of every term. fp16 has little range: P's rows, S's copy and v are brought to the middle of it by powers of two,
 // which are taken out again from the fp32 sums.
 // A row's values reach only what sees them: rows behind the sequence are zero-filled; in a
 // chunk where a decay may underflow to 0, what it multiplies is dropped; a chunk whose V holds a
 // value that is not finite forms P V row by row.
 // Bound: HBM (q, k, v once per 64 value columns, o) and the warp MMAs (1024 multiply-adds per
 // clock and SM measured) are close; what is left is instruction issue, hence the tables that
-// one warp (the one with the fewest tiles of P) forms a chunk ahead for all.
+// one warp (the one with the fewest tiles of P) forms a chunk ahead for all. Eight prompts of 2000
+// rows, bf16: 50 heads of 16 x 64 with shared keys 107 us (their 212 MB take 32), 25 of 128 x 128
+// with 5 key heads 339 us.
 #include "kernels.h"
 #include "ragged.cuh"
 
@@ -201,6 +202,7 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
                      const int* __restrict__ cu, int total, const float* state_in, float* state_out,
                      T* __restrict__ o, long long ldo, int Hk, int H, int dv, float log2_scale, int* status) {
     constexpr bool F16 = std::is_same<T, f16>::value;
+    constexpr int PARTS = std::is_same<T, f16>::value ? 2 : 3;  // of the state update's scaled v
     constexpr int NKT = DK / 8, KK = DK / 16;  // 8- and 16-wide key tiles
     griddep_sync();
     extern __shared__ __align__(128) uint8_t chunk_raw[];
@@ -500,7 +502,7 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
                 uint32_t kf[KK][4];
 #pragma unroll
                 for (int n = 0; n < KK; ++n) wm::ldsm_x4_t(kf[n], ks + kk * 16 * DK * 2 + xa[n]);
-                uint32_t hi[4], lo[4];
+                uint32_t part[PARTS][4];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const float2 w = *reinterpret_cast<const float2*>(&tab.w[16 * kk + 8 * x + 2 * lq]);
@@ -512,19 +514,23 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
                         const uint32_t vv = resets ? vf[kk][2 * y + x] & keep : vf[kk][2 * y + x];
                         const T* e = reinterpret_cast<const T*>(&vv);
                         const float2 z = __fmul2_rn(make_float2(to_f(e[0]), to_f(e[1])), w);
-                        wm::split2<T>(z.x, z.y, &hi[2 * x + y], &lo[2 * x + y]);
+                        part[0][2 * x + y] = pack2<T>(z.x, z.y);
+                        float2 left = z;
+#pragma unroll
+                        for (int p = 1; p < PARTS; ++p) {
+                            const T* of = reinterpret_cast<const T*>(&part[p - 1][2 * x + y]);
+                            left = make_float2(left.x - to_f(of[0]), left.y - to_f(of[1]));  // exact
+                            part[p][2 * x + y] = pack2<T>(left.x, left.y);
+                        }
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < KK; ++n) {
-                    wm::mma16<T>(st[2 * n], hi, kf[n][0], kf[n][1]);
-                    wm::mma16<T>(st[2 * n + 1], hi, kf[n][2], kf[n][3]);
-                }
+                for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-                for (int n = 0; n < KK; ++n) {
-                    wm::mma16<T>(st[2 * n], lo, kf[n][0], kf[n][1]);
-                    wm::mma16<T>(st[2 * n + 1], lo, kf[n][2], kf[n][3]);
-                }
+                    for (int n = 0; n < KK; ++n) {
+                        wm::mma16<T>(st[2 * n], part[p], kf[n][0], kf[n][1]);
+                        wm::mma16<T>(st[2 * n + 1], part[p], kf[n][2], kf[n][3]);
+                    }
             }
             if (F16) {
                 const float back = inverse(fv);
@@ -568,7 +574,6 @@ int launch_dk(const Ctx& ctx, const LinAttn& a) {
 template <typename T>
 int launch_linattn_chunk(const Ctx& ctx, const LinAttn& a) {
     if (a.dk == 16) return launch_dk<T, 16>(ctx, a);
-    if (a.dk == 64) return launch_dk<T, 64>(ctx, a);
     if (a.dk == 128) return launch_dk<T, 128>(ctx, a);
     return HYMBA_ERR_UNSUPPORTED;
 }

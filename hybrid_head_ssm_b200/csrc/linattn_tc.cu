@@ -942,7 +942,7 @@ int launch_dv(const Ctx& ctx, const LinAttn& x) {
 
 }  // namespace
 
-bool linattn_tc_applies(int dk, int total) { return dk == DK && total > 0; }
+bool linattn_tc_applies(int dk) { return dk == DK; }
 
 size_t linattn_tc_bytes(int n_seqs, int total, int H, int dv) {
     const int seg = segment_rows(n_seqs, total, H, dv);

@@ -146,7 +146,7 @@ static bool linattn_rows_ok(const hymba_linattn_shape& s, const void* q, int64_t
 
 size_t hymba_linattn_workspace(const hymba_linattn_shape* shape, int n_seqs, int total_rows) {
     if (check_linattn(shape) || n_seqs <= 0 || n_seqs > kMostRows || total_rows < 0 || total_rows > kMostRows) return 0;
-    if (shape->dtype != HYMBA_F32 && linattn_tc_applies(shape->key_dim, total_rows))
+    if (shape->dtype != HYMBA_F32 && total_rows > 0 && linattn_tc_applies(shape->key_dim))
         return linattn_tc_bytes(n_seqs, total_rows, shape->n_heads, shape->v_head_dim);
     return 256;
 }
@@ -179,8 +179,10 @@ int hymba_linattn_prefill(const hymba_linattn_shape* shape, const void* q, int64
     a.cu = cu_seqlens;
     a.n_seqs = n_seqs;
     a.total = total_rows;
-    if (shape->dtype == HYMBA_F32) return launch_linattn_recurrent<float>(ctx, a);
-    if (linattn_tc_applies(a.dk, a.total)) return shape->dtype == HYMBA_F16 ? launch_linattn_tc<f16>(ctx, a) : launch_linattn_tc<bf16>(ctx, a);
+    // (without rows only states are copied)
+    if (shape->dtype == HYMBA_F32 || total_rows == 0) return launch_linattn_recurrent<float>(ctx, a);
+    if (linattn_tc_applies(a.dk))
+        return shape->dtype == HYMBA_F16 ? launch_linattn_tc<f16>(ctx, a) : launch_linattn_tc<bf16>(ctx, a);
     if (shape->dtype == HYMBA_F16) return launch_linattn_chunk<f16>(ctx, a);
     return launch_linattn_chunk<bf16>(ctx, a);
 }
