@@ -62,6 +62,18 @@ attn_packed_simt_kernel(const T* __restrict__ q, long long ldq, const T* __restr
     k += row0 * ldk + (long long)g * DH;
     v += row0 * ldv + (long long)g * DV;
 
+    const int i_last = min(i0 + QT, L) - 1;
+    const int lo = window > 0 ? max(n_meta, i0 - window + 1) : n_meta;
+    // key tiles: the meta range, then the window's; first key j0 of the range's `end`
+    int range = 0, j0 = 0, end = min(n_meta, i_last + 1);
+    auto settle = [&] {  // to the window's range when the meta range is done; false: no tile is left
+        if (range == 0 && j0 >= end) {
+            range = 1;
+            j0 = lo;
+            end = i_last + 1;
+        }
+        return j0 < end;
+    };
     for (int j = tid; j < QT * (DH / 8); j += NT) {
         const int r = j % QT, c = j / QT;
         float x[8];
@@ -78,107 +90,125 @@ attn_packed_simt_kernel(const T* __restrict__ q, long long ldq, const T* __restr
 #pragma unroll
         for (int c = 0; c < DV / 32; ++c) acc[r][c] = make_float2(0.f, 0.f);
     }
-    const int i_last = min(i0 + QT, L) - 1;
-    const int lo = window > 0 ? max(n_meta, i0 - window + 1) : n_meta;
-    for (int range = 0; range < 2; ++range) {
-        const int end = range == 0 ? min(n_meta, i_last + 1) : i_last + 1;
-        for (int j0 = range == 0 ? 0 : lo; j0 < end; j0 += KT) {
-            __syncthreads();
-            int odd = 0;  // a value of V that is not finite: the product may not meet it where it is masked
-            for (int j = tid; j < KT * (DH / 8); j += NT) {
-                const int r = j % KT, c = j / KT;
-                float x[8] = {};
-                if (j0 + r < end) ragged::load8(k + (long long)(j0 + r) * ldk + 8 * c, x);
+    // this thread's pieces of a tile's K (8 values of one row each) and V: all loads in flight at once
+    // (a loop of load and store: 61 us against 54 for 4 prompts of up to 3000 rows)
+    constexpr int NKP = KT * (DH / 8) / NT, NVP = KT * (DV / 8) / NT;
+    while (settle()) {
+        float kx[NKP][8], vx[NVP][8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sm.k[8 * c + e][r] = x[e];
+        for (int x = 0; x < NKP; ++x) {
+            const int j = tid + x * NT, r = j % KT, c = j / KT;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kx[x][e] = 0.f;
+            if (j0 + r < end) ragged::load8(k + (long long)(j0 + r) * ldk + 8 * c, kx[x]);
+        }
+#pragma unroll
+        for (int x = 0; x < NVP; ++x) {
+            const int j = tid + x * NT, c = j % (DV / 8), r = j / (DV / 8);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) vx[x][e] = 0.f;
+            if (j0 + r < end) ragged::load8(v + (long long)(j0 + r) * ldv + 8 * c, vx[x]);
+        }
+        __syncthreads();
+        int odd = 0;  // a value of V that is not finite: the product may not meet it where it is masked
+#pragma unroll
+        for (int x = 0; x < NKP; ++x) {
+            const int j = tid + x * NT, r = j % KT, c = j / KT;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sm.k[8 * c + e][r] = kx[x][e];
+        }
+#pragma unroll
+        for (int x = 0; x < NVP; ++x) {
+            const int j = tid + x * NT, c = j % (DV / 8), r = j / (DV / 8);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) odd |= !isfinite(vx[x][e]);
+            *reinterpret_cast<float4*>(&sm.v[r][8 * c]) = make_float4(vx[x][0], vx[x][1], vx[x][2], vx[x][3]);
+            *reinterpret_cast<float4*>(&sm.v[r][8 * c + 4]) = make_float4(vx[x][4], vx[x][5], vx[x][6], vx[x][7]);
+        }
+        odd = __syncthreads_or(odd);
+        const int at = j0, to = end;
+        const bool meta = range == 0;
+        j0 += KT;
+        float2 s2[RT][2];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s2[r][0] = s2[r][1] = make_float2(0.f, 0.f);
+#pragma unroll 16
+        for (int d = 0; d < DH; ++d) {
+            float av[RT];
+            row_values<RT>(&sm.q[d][RT * ty], av);
+            const float4 b = *reinterpret_cast<const float4*>(&sm.k[d][4 * tx]);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const float2 a2 = make_float2(av[r], av[r]);
+                s2[r][0] = __ffma2_rn(a2, make_float2(b.x, b.y), s2[r][0]);
+                s2[r][1] = __ffma2_rn(a2, make_float2(b.z, b.w), s2[r][1]);
             }
-            for (int j = tid; j < KT * (DV / 8); j += NT) {
-                const int c = j % (DV / 8), r = j / (DV / 8);
-                float x[8] = {};
-                if (j0 + r < end) ragged::load8(v + (long long)(j0 + r) * ldv + 8 * c, x);
+        }
+        float s[RT][4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) odd |= !isfinite(x[e]);
-                *reinterpret_cast<float4*>(&sm.v[r][8 * c]) = make_float4(x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<float4*>(&sm.v[r][8 * c + 4]) = make_float4(x[4], x[5], x[6], x[7]);
+        for (int r = 0; r < RT; ++r) {
+            s[r][0] = s2[r][0].x;
+            s[r][1] = s2[r][0].y;
+            s[r][2] = s2[r][1].x;
+            s[r][3] = s2[r][1].y;
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const int i = i0 + RT * ty + r;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int j = at + 4 * tx + c;
+                const bool see = j < to && j <= i && (meta || window <= 0 || i - j < window);
+                s[r][c] = see ? s[r][c] : -INFINITY;
+                mx = fmaxf(mx, s[r][c]);
             }
-            odd = __syncthreads_or(odd);
-            float2 s2[RT][2];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) s2[r][0] = s2[r][1] = make_float2(0.f, 0.f);
-#pragma unroll 8
-            for (int d = 0; d < DH; ++d) {
-                float av[RT];
-                row_values<RT>(&sm.q[d][RT * ty], av);
-                const float4 b = *reinterpret_cast<const float4*>(&sm.k[d][4 * tx]);
+            for (int w = 1; w < 16; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+            const float m = fmaxf(mrun[r], mx), mu = m == -INFINITY ? 0.f : m;
+            const float f = exp2f(mrun[r] - mu);
+            mrun[r] = m;
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                s[r][c] = exp2f(s[r][c] - mu);
+                sum += s[r][c];
+            }
+            l[r] = l[r] * f + sum;  // this thread's columns; the 16 threads of the row are added at the end
+#pragma unroll
+            for (int c = 0; c < DV / 32; ++c) acc[r][c] = __fmul2_rn(acc[r][c], make_float2(f, f));
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) sm.p[4 * tx + c][RT * ty + r] = s[r][c];
+        __syncthreads();
+        const int nk = min(KT, to - at);
+        auto add = [&](int j, bool all) {
+            float av[RT];
+            row_values<RT>(&sm.p[j][RT * ty], av);
+#pragma unroll
+            for (int u = 0; u < DV / 64; ++u) {
+                const float4 b = *reinterpret_cast<const float4*>(&sm.v[j][4 * tx + 64 * u]);
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
+                    const int i = i0 + RT * ty + r, jj = at + j;
+                    if (!all && !(jj <= i && (meta || window <= 0 || i - jj < window))) continue;
                     const float2 a2 = make_float2(av[r], av[r]);
-                    s2[r][0] = __ffma2_rn(a2, make_float2(b.x, b.y), s2[r][0]);
-                    s2[r][1] = __ffma2_rn(a2, make_float2(b.z, b.w), s2[r][1]);
+                    acc[r][2 * u] = __ffma2_rn(a2, make_float2(b.x, b.y), acc[r][2 * u]);
+                    acc[r][2 * u + 1] = __ffma2_rn(a2, make_float2(b.z, b.w), acc[r][2 * u + 1]);
                 }
             }
-            float s[RT][4];
+        };
+        if (odd) {
+            for (int j = 0; j < nk; ++j) add(j, false);
+        } else {
+            // (rows of V behind the tile's last key are zero, and so are their weights)
+            const int n8 = (nk + 7) & ~7;
+#pragma unroll 1
+            for (int j = 0; j < n8; j += 8)
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                s[r][0] = s2[r][0].x;
-                s[r][1] = s2[r][0].y;
-                s[r][2] = s2[r][1].x;
-                s[r][3] = s2[r][1].y;
-            }
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const int i = i0 + RT * ty + r;
-                float mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int j = j0 + 4 * tx + c;
-                    const bool see = j < end && j <= i && (range == 0 || window <= 0 || i - j < window);
-                    s[r][c] = see ? s[r][c] : -INFINITY;
-                    mx = fmaxf(mx, s[r][c]);
-                }
-#pragma unroll
-                for (int w = 1; w < 16; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-                const float m = fmaxf(mrun[r], mx), mu = m == -INFINITY ? 0.f : m;
-                const float f = exp2f(mrun[r] - mu);
-                mrun[r] = m;
-                float sum = 0.f;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    s[r][c] = exp2f(s[r][c] - mu);
-                    sum += s[r][c];
-                }
-                l[r] = l[r] * f + sum;  // this thread's columns; the 16 threads of the row are added at the end
-#pragma unroll
-                for (int c = 0; c < DV / 32; ++c) acc[r][c] = __fmul2_rn(acc[r][c], make_float2(f, f));
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int r = 0; r < RT; ++r) sm.p[4 * tx + c][RT * ty + r] = s[r][c];
-            __syncthreads();
-            const int nk = min(KT, end - j0);
-#pragma unroll 4
-            for (int j = 0; j < nk; ++j) {
-                float av[RT];
-                row_values<RT>(&sm.p[j][RT * ty], av);
-                bool see[RT];
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const int i = i0 + RT * ty + r, jj = j0 + j;
-                    see[r] = !odd || (jj <= i && (range == 0 || window <= 0 || i - jj < window));
-                }
-#pragma unroll
-                for (int u = 0; u < DV / 64; ++u) {
-                    const float4 b = *reinterpret_cast<const float4*>(&sm.v[j][4 * tx + 64 * u]);
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        if (!see[r]) continue;
-                        const float2 a2 = make_float2(av[r], av[r]);
-                        acc[r][2 * u] = __ffma2_rn(a2, make_float2(b.x, b.y), acc[r][2 * u]);
-                        acc[r][2 * u + 1] = __ffma2_rn(a2, make_float2(b.z, b.w), acc[r][2 * u + 1]);
-                    }
-                }
-            }
+                for (int x = 0; x < 8; ++x) add(j + x, true);
         }
     }
 #pragma unroll
@@ -215,8 +245,8 @@ int launch_tile(const Ctx& ctx, const PackedAttn& a) {
 
 // The smallest tile whose blocks still fit one wave of the 148 SMs (a block's time is a chain of
 // key tiles, shorter with fewer rows), 64 rows where none does. 4 heads of 64 x 128: prompts of
-// 272 and 141 rows 15.8 us in tiles of 16, 19.6 in 32, 31.2 in 64; one of 700 rows 24.0 in 16 (a
-// second wave), 19.8 in 32, 31.2 in 64.
+// 272 and 141 rows 14.1 us in tiles of 16, 16.6 in 32, 20.5 in 64; one of 700 rows 23.8 in 16 (a
+// second wave), 16.7 in 32, 20.6 in 64; two of up to 1000 38.4 in 32, 20.7 in 64.
 template <typename T, int DH, int DV>
 int launch_dims(const Ctx& ctx, const PackedAttn& a) {
     auto blocks = [&](int qt) { return ((long long)ceil_div(a.total, qt) + a.n_seqs) * a.H; };

@@ -6,7 +6,8 @@
 // State S [v_head_dim, key_dim] fp32 per (sequence, head). A warp owns VR consecutive rows
 // of S in registers: LPR lanes per row, each with every LPR-th float4 of the key
 // dimension, so a warp's loads are whole 128-byte lines and a row's product with q is a
-// shuffle over LPR lanes. Single tokens are bound by HBM: 8 bytes per state element.
+// shuffle over LPR lanes. Single tokens are bound by HBM: 8 bytes per state element; 256 of 25
+// heads of 64 x 128 63.5 us (the copy rate), one 2.2 us.
 #include "kernels.h"
 #include "ragged.cuh"
 

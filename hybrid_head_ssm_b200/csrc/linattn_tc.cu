@@ -35,7 +35,9 @@
 // each segment, and the segments then run side by side.
 // A CTA that noted a value of V that is not finite computes its rows once more by the
 // recurrence, in which nothing reaches a row that does not see it.
-// Bound: HBM (q, k, v read and o written once per 128 value columns).
+// Bound: HBM (q, k, v read and o written once per 128 value columns); what is left is the chain of a
+// chunk, about 6900 clocks, and the last sequences' chunks alone. Eight prompts of up to 4224 rows
+// (19800 in all), 25 heads of 64 x 128, bf16: 124 us, 49% of the copy rate.
 #include <algorithm>
 
 #include "attn_tile.cuh"

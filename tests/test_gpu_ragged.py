@@ -411,6 +411,26 @@ def test_append_paged(dt, page):
     assert (_np(kv.k_pages) == kw).all() and (_np(kv.v_pages) == vw).all()
 
 
+@pytest.mark.parametrize("batch", [33, 1100])
+def test_append_paged_many_sequences(batch):
+    """More sequences than a warp looks through at once (twice over), every third without new rows,
+    rows wider than a warp takes in one go, rows behind the last sequence left alone."""
+    torch, hy, rt, code, tdt = _mods()
+    G, dh, dv, page = 7, 128, 128, 4
+    lens = [1 + (5 * b) % 9 for b in range(batch)]
+    new = [0 if b % 3 == 1 else min(n, 1 + b % 2) for b, n in enumerate(lens)]
+    kv = _cache("bf16", lens, G, dh, dv, page, 44)
+    rows = sum(new) + 5
+    k = torch.randn(rows, G * dh, device="cuda").to(torch.bfloat16)
+    v = torch.randn(rows, G * dv, device="cuda").to(torch.bfloat16)
+    cu = _offsets(new)
+    k0, v0, table = _np(kv.k_pages), _np(kv.v_pages), kv.page_table.cpu().numpy()
+    rt.kv_append_paged(kv, k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    _status_ok(hy, torch)
+    kw, vw = ro.append_pages(k0, v0, table, lens, _np(k), _np(v), cu)
+    assert (_np(kv.k_pages) == kw).all() and (_np(kv.v_pages) == vw).all()
+
+
 def test_append_paged_out_of_range():
     """A page outside the pool, more rows than positions, a length past the table, offsets
     out of order: those rows are left out, the others written."""
