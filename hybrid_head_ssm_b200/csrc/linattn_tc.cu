@@ -875,16 +875,18 @@ __global__ void __launch_bounds__(256) linattn_starts_kernel(const Args a) {
 }
 
 // How sequences are cut where they and their heads leave SMs idle: 0 (whole), or rows per segment
-// such that the segments' blocks fill the GPU once. Two more launches and a second look at k and v
-// ask for at least three segments, of at least three chunks. bf16, heads of 64 x 128, cut and
-// whole: one prompt of 8192 rows and 25 heads 90 and 194 us, of 2000 rows 37 and 52 us; of 30,000
-// rows and 8 heads 103 and 678 us; three of 3000, 2500 and 10 rows and 8 heads 36 and 76 us.
+// such that the segments' blocks fill the GPU once, three chunks at least. A chunk costs about two
+// thirds as much again in the pass over states, the launches and the join as much as 400 rows: that
+// has to pay also where all sequences are equally long, which the host does not know. bf16,
+// heads of 64 x 128, cut and whole: one prompt of 8192 rows, 25 heads 90 and 194 us, 73 heads 191
+// and 196; of 1100 rows, 8 heads 29 and 32 (1000 rows would be even); of 30,000 rows 102 and 677; 8
+// heads, four prompts of 2000 rows 44 and 53, one of 9000 and three of 1000 59 and 214.
 int segment_rows(int n_seqs, int total, int H, int dv) {
     const long long per = (long long)H * (dv % 128 ? dv / 64 : dv / 128);  // blocks of a segment
     const long long want = 148 / per - (n_seqs - 1);  // segments of n sequences: up to n - 1 more than of one
-    if (n_seqs > 32 || want < 3) return 0;
+    if (n_seqs > 32 || want < 2) return 0;
     const long long rows = std::max<long long>(3 * CQ, round_up((total + want - 1) / want, CQ));
-    return total <= 2 * rows || total < 9 * CQ ? 0 : (int)rows;
+    return n_seqs * (rows + rows * 2 / 3 + 400) < total ? (int)rows : 0;
 }
 long long segment_items(int seg, int n_seqs, int total) { return (total + seg - 1) / seg + n_seqs - 1; }
 

@@ -273,6 +273,8 @@ def _decays(g: torch.Tensor, rows: int, heads: int, dev: torch.device) -> int:
 
 
 def linattn_workspace(shape, n_seqs: int, rows: int, device="cuda") -> torch.Tensor:
+    """Scratch for linattn_prefill calls with just these numbers of sequences and rows (fewer may
+    need more: few long prompts are cut into segments)."""
     n = hymba_linattn_workspace(ctypes.byref(shape), n_seqs, rows)
     _need(n > 0, "invalid linear-attention shape, sequence count or row count")
     return torch.empty(n, dtype=torch.uint8, device=device)

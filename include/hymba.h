@@ -401,8 +401,9 @@ int hymba_kv_append_paged(const hymba_paged_kv* kv, const void* k, int64_t ldk, 
  * the cache's (HYMBA_ERR_KV_INCOMPATIBLE). The keys are split over blocks by max_len and
  * the batch; the partial results meet in `workspace` (256-byte aligned, at least
  * hymba_attn_decode_paged_workspace(shape, batch, max_len) bytes with the same max_len
- * as the call, or its page capacity where the call passes 0; contents are undefined
- * before and after; calls that may overlap need workspaces of their own). */
+ * as the call, or its page capacity where the call passes 0; a smaller batch is split
+ * further and may need more; contents are undefined before and after; calls that may
+ * overlap need workspaces of their own). */
 int hymba_attn_decode_paged(const hymba_attn_shape* shape, const void* q, int64_t ldq, const hymba_paged_kv* kv,
                             int max_len, void* o, int64_t ldo, void* workspace, size_t ws_bytes, void* stream);
 /* Bytes of that workspace (0 if an argument is invalid). */
@@ -436,7 +437,9 @@ int hymba_linattn_prefill(const hymba_linattn_shape* shape, const void* q, int64
                           const void* v, int64_t ldv, const float* g, int64_t ldg, const int32_t* cu_seqlens,
                           int n_seqs, int total_rows, const float* state_in, float* state_out, void* o, int64_t ldo,
                           void* workspace, size_t ws_bytes, void* stream);
-/* Bytes of that workspace (0 if an argument is invalid). */
+/* Bytes of that workspace (0 if an argument is invalid), for a call with just these numbers:
+ * few long sequences are cut into segments whose states meet there, so a call with fewer
+ * sequences or rows may need more. */
 size_t hymba_linattn_workspace(const hymba_linattn_shape* shape, int n_seqs, int total_rows);
 
 /* One token per sequence: row b of q, k, v, g and o belongs to state[b], which is updated in

@@ -656,7 +656,8 @@ def test_linear_attention_offsets_out_of_order_are_left_out(dt):
 # few long prompts, whose rows several blocks share
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("lens,heads,dims", [([1409], (1, 1), (64, 64)), ([0, 1300, 1, 900, 384], (2, 4), (64, 128)),
-                                             ([2304, 2305], (3, 3), (64, 192)), ([1152] + [0] * 31, (1, 2), (64, 128))])
+                                             ([2304, 2305], (3, 3), (64, 192)), ([1152] + [0] * 31, (1, 2), (64, 128)),
+                                             ([0, 4100, 1, 900, 384], (1, 2), (64, 64)), ([5, 0, 0, 5000], (2, 2), (64, 128))])
 @pytest.mark.parametrize("start", [False, True])
 def test_linear_attention_few_long_prompts(dt, lens, heads, dims, start):
     torch, hy, rt, code, tdt = _mods()
@@ -680,7 +681,7 @@ def test_linear_attention_few_long_prompts_non_finite(dt):
     """A NaN in the second segment of a long prompt, and a reset two segments later: rows before
     the one and behind the other keep their values."""
     torch, hy, rt, code, tdt = _mods()
-    lens, Hk, H, dk, dv = [1800, 30], 2, 2, 64, 64
+    lens, Hk, H, dk, dv = [2500, 30], 2, 2, 64, 64
     x = _linear(dt, lens, Hk, H, dk, dv, 57, decay=0.01)
     q, k, v, g, st, cu = x
     n, at, reset = sum(lens), 500, 1300
@@ -704,8 +705,8 @@ def test_linear_attention_few_long_prompts_offsets_out_of_order():
     """More segments than the offsets may name: nothing outside the buffers is touched."""
     torch, hy, rt, code, tdt = _mods()
     Hk, H, dk, dv = 2, 2, 64, 64
-    x = list(_linear("bf16", [1500, 100, 100], Hk, H, dk, dv, 58, pad=0))
-    x[5] = torch.tensor([0, 1700, 0, 1700], dtype=torch.int32, device="cuda")
+    x = list(_linear("bf16", [5000, 100, 100], Hk, H, dk, dv, 58, pad=0))
+    x[5] = torch.tensor([0, 5200, 0, 5200], dtype=torch.int32, device="cuda")
     o, end = _run_linear("bf16", x, Hk, H, dk, dv, True)
     _status_range(hy, torch)
     assert end[1].isnan().all()  # the one with a negative length, not written

@@ -257,6 +257,26 @@ def test_linear_attention_arguments_refused(hy):
         assert hy.hymba_linattn_workspace(ctypes.byref(s), n, rows) == 0
 
 
+def test_linear_attention_workspace_of_few_long_prompts(hy):
+    """One long prompt of 16-bit rows is cut, and its segments' states need room; short ones, many
+    sequences, enough heads, fp32 rows and other key dims need none. A call with too little is
+    refused, also where a larger batch would have needed less."""
+    ws = lambda s, n, rows: hy.hymba_linattn_workspace(ctypes.byref(s), n, rows)
+    H, dk, dv = 4, 64, 128
+    state = H * dk * dv * 4
+    s = hy.linattn_shape(2, H, dk, dv, hy.HYMBA_BF16)
+    for n, rows in ((1, 8192), (3, 5000), (4, 20000)):
+        assert 3 * state < ws(s, n, rows) < 148 * (state + H * 4) + 256, (n, rows)
+    for n, rows in ((1, 0), (1, 300), (1, 1000), (8, 8000), (33, 100000), (500, 1 << 30)):
+        assert ws(s, n, rows) == 256, (n, rows)
+    for other in (hy.linattn_shape(2, H, dk, dv, hy.HYMBA_F32), hy.linattn_shape(2, H, 16, dv, hy.HYMBA_BF16),
+                  hy.linattn_shape(2, H, 128, dv, hy.HYMBA_F16), hy.linattn_shape(75, 75, dk, dv, hy.HYMBA_F16)):
+        assert ws(other, 1, 8192) == 256
+    s = _lin(hy, dtype=hy.HYMBA_F16)
+    assert _lin_prefill(hy, s, n=1, rows=8192, nws=ws(s, 40, 8192)) == hy.HYMBA_ERR_WORKSPACE_TOO_SMALL
+    assert _lin_prefill(hy, s, n=1, rows=8192, nws=ws(s, 1, 8192) - 1) == hy.HYMBA_ERR_WORKSPACE_TOO_SMALL
+
+
 # ------------------------------------------------------------------ the torch helpers
 def test_helpers_refuse_tensors_that_do_not_fit(hy):
     import torch
