@@ -19,11 +19,13 @@
 //               and noted;
 //   warps 4-7   softmax of tile A, warps 8-11 of tile B: one thread per query row. P =
 //               2^(s - m) as 16-bit pairs, the row sum of the fp32 values; O is rescaled in
-//               TMEM only when the running max grows by more than 2^8.
+//               TMEM only when the running max grows by more than 2^4 (fp16) or 2^8 (bf16).
 // A CTA that noted a value that is not finite computes its rows once more from global
 // memory, key by key over what each row sees.
 // P is rounded to the rows' type, as an MMA operand has to be: half a step relative to each
-// weight, the size of the output's own rounding.
+// weight, the size of the output's own rounding. fp16 has little range: m is the running max less
+// 11, so that P lies between 2^11 and 2^15 at the largest weight and keeps all its bits down to
+// 2^-25 of it (below, half of fp16's smallest step: 2^-36 of it); the factor leaves with the row sum.
 // Bound by the tensor cores (2 (dh + dv) flops per visible pair); what is left is the softmax's
 // instruction issue, about 1500 clocks per 64 keys and tile with two tiles on the SM's four
 // schedulers, and in windows a block's start and end, about 10,000 clocks. 25 heads of 64 x 128:
@@ -45,7 +47,13 @@ constexpr int REG_SOFT = 216, REG_OTHER = 64;
 // the launch allocates 168 registers per thread (65536 / 384, rounded down to 8): the
 // split must fit that pool (the launcher also checks the compiled count)
 static_assert(4 * 32 * REG_OTHER + 8 * 32 * REG_SOFT <= NT * 168, "register split exceeds the launch's pool");
-constexpr float RESCALE_LOG2 = 8.0f;
+// m is the running max (log2 units) less LOW; it moves when a score passes it by more than TOP.
+// fp16: 2^15 is the largest power of two there is; bf16 has fp32's range
+template <typename T>
+struct Weights {
+    static constexpr float LOW = std::is_same<T, bf16>::value ? 0.f : 11.f;
+    static constexpr float TOP = std::is_same<T, bf16>::value ? 8.f : 15.f;
+};
 // TMEM columns: O_A [0,128), O_B [128,256), S_A [256,384), S_B [384,512); P_t in the first
 // 64 columns of S_t (128 16-bit keys per row, two per column)
 constexpr uint32_t TM_O = 0, TM_S = 256;
@@ -144,7 +152,7 @@ __device__ __forceinline__ uint32_t drop_odd(uint32_t w) {
     return w & ~__vcmpeq2(w & E, E);
 }
 
-// One row from global memory over exactly the keys it sees, with the row's max and sum.
+// One row from global memory over exactly the keys it sees, with the row's m and sum.
 template <typename T, int DH, int DV>
 __device__ __noinline__ void recompute_row(const T* q, const T* k, long long ldk, const T* v, long long ldv, T* o, int i,
                                            int n_meta, int window, float scale, float mu, float inv) {
@@ -458,17 +466,18 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
             for (int y = 0; y < 8; ++y) mx8[y] = fmaxf(mx8[y], sv[KS - 8 + y]);
             const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                                    fmaxf(mx8[6], mx8[7])) * scale;
-            // a row whose running max grows by more than 2^8 moves to the new max, and its O is
+            // a row whose running max has grown too far moves to the new max, and its O is
             // scaled in TMEM, between the products of the step before and of this one
             float f = 1.f;
             bool scale_o = false;
-            if (mx > m_used + RESCALE_LOG2) {
+            if (mx > m_used + Weights<T>::TOP) {
+                const float to = mx - Weights<T>::LOW;
                 if (m_used != -INFINITY) {
-                    f = exp2f(m_used - mx);
+                    f = exp2f(m_used - to);
                     l *= f;
                     scale_o = true;
                 }
-                m_used = mx;
+                m_used = to;
             }
             // P = 2^(s * scale - m) in fp32, summed in fp32, stored as 16-bit pairs
             const float mu = m_used == -INFINITY ? 0.f : m_used;
