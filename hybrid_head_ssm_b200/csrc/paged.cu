@@ -262,12 +262,19 @@ __global__ void __launch_bounds__(128) decode_paged_simt_kernel(const DecodeArgs
 // another until the split ends; 96 KB of ring per block keeps two blocks per SM and about
 // 150 KB per SM in flight. Per tile: S^T = K q^T (keys x heads, K by ldmatrix, q as the B
 // operand in registers), p = 2^(s - m) with O rescaled only when a max grows by more than
-// 2^8, and O^T += V^T P^T (V^T by transposing ldmatrix, P^T by an 8 x 8 register transpose).
-// p enters the product as two 16-bit parts (p = hi + lo), so the weights keep 16 bits or
-// more. Slots are looked up one tile ahead of their copies: lane i holds key i's row. Rows
-// past the split's last key are zero-filled by the copy and masked. Bound by HBM: K and V
-// of every visible key once.
+// 2^4 (fp16) or 2^8 (bf16), and O^T += V^T P^T (V^T by transposing ldmatrix, P^T by an 8 x 8
+// register transpose). p enters the product as two 16-bit parts (p = hi + lo), so the weights keep
+// 16 bits or more; in fp16 m is the running max less 11, so that they do so down to 2^-20 of the
+// largest (below, half of fp16's smallest step: 2^-36 of it). Slots are looked up one tile
+// ahead of their copies: lane i holds key i's row. Rows past the split's last key are
+// zero-filled by the copy and masked. Bound by HBM: K and V of every visible key once.
 constexpr int TK = 16;                 // keys per tile
+// m is the running max (log2 units) less LOW; it moves when a score passes it by more than TOP
+template <typename T>
+struct Weights {
+    static constexpr float LOW = std::is_same<T, f16>::value ? 11.f : 0.f;
+    static constexpr float TOP = std::is_same<T, f16>::value ? 15.f : 8.f;
+};
 // Three blocks per SM with 72 KB (64 KB) of rings each where a tile has at most 192 (128)
 // dims, two with 96 KB at 256. 64 sequences of the 1.5B heads, window 1024: 33.0 us against 36.0
 // with two blocks of four stages; 16 long contexts 100.9 against 115.4.
@@ -403,11 +410,11 @@ __global__ void __launch_bounds__(128, blocks_per_sm(DH + DV, NG)) decode_paged_
             }
             mx[0] *= a.scale_log2;
             mx[1] *= a.scale_log2;
-            if (__any_sync(0xffffffffu, mx[0] > m[n][0] + 8.f || mx[1] > m[n][1] + 8.f)) {
+            if (__any_sync(0xffffffffu, mx[0] > m[n][0] + Weights<T>::TOP || mx[1] > m[n][1] + Weights<T>::TOP)) {
                 float f[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float to = fmaxf(m[n][e], mx[e]);
+                    const float to = fmaxf(m[n][e], mx[e] - Weights<T>::LOW);
                     f[e] = to == -INFINITY ? 1.f : fast_exp2(m[n][e] - to);
                     m[n][e] = to;
                     l[n][e] *= f[e];

@@ -5,12 +5,13 @@ numbers. Bounds are those of test_gpu_ragged.py; where a test adds to one, its d
 import numpy as np
 import pytest
 
-from test_gpu_ragged import _attn_bound, _hold, _mods, _np, _packed, _status_ok
+from oracle import ragged_oracle as ro
+from test_gpu_ragged import TINY, U, _attn_bound, _cache, _decode, _hold, _mods, _np, _packed, _status_ok
 
 pytestmark = pytest.mark.gpu
 
 
-def _sink(q, k, v, rows, sink, gap, dh):
+def _sink(q, k, v, sink, gap, dh):
     """Scores 0 at the sink key, -gap (log2) at all others; V 0 at the sink and about 1 elsewhere."""
     q.zero_()
     q[:, ::dh] = 1.0
@@ -32,7 +33,7 @@ def test_packed_attention_long_tail_behind_a_sink(dt, gap, at):
     torch, hy, rt, code, tdt = _mods()
     H, G, dh, dv, L = 2, 1, 64, 64, 4001
     q, k, v, cu = _packed(dt, [L], H, G, dh, dv, 201, pad=0)
-    _sink(q, k, v, L, [at], gap, dh)
+    _sink(q, k, v, [at], gap, dh)
     o = torch.zeros(L, H * dv, dtype=tdt[dt], device="cuda")
     rt.attn_prefill_packed(hy.attn_shape(H, G, dh, dv, 0, 0, code[dt], 1.0), q, k, v, cu, o)
     _status_ok(hy, torch)
@@ -45,3 +46,33 @@ def test_packed_attention_long_tail_behind_a_sink(dt, gap, at):
         want[x] = np.tile(p @ vv[:i + 1] / p.sum(), H)
     big = np.full((len(rows), H), 18.1)  # scale |q||k|
     _hold(_np(o)[rows], want, _attn_bound(want, want, big, dt, dh, dv, L, 1.0), f"{dt} 2^-{gap}")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("gap", [8, 16, 20, 24, 26])
+@pytest.mark.parametrize("at", [0, 700])
+def test_decode_paged_long_tail_behind_a_sink(dt, gap, at):
+    """As above, one token over the pages, in a batch whose sequences are not split: the warp that meets
+    the sink has a quarter of the tail. All sequences share their pages. Weights keep 16 bits or
+    more (fp16's at 2^-24 and 2^-26 of the largest 12 and 10, whose half steps lie below 2^-11)."""
+    torch, hy, rt, code, tdt = _mods()
+    B, H, G, dh, dv, L, page = 160, 8, 8, 64, 64, 1201, 32
+    kv = _cache(dt, [L] + [1] * (B - 1), G, dh, dv, page, 202)
+    kv.page_table[:] = kv.page_table[0]
+    kv.len.fill_(L)
+    pages = kv.page_table[0].long()
+    k = torch.zeros(L, G * dh, dtype=tdt[dt], device="cuda")
+    v = torch.randn(L, G * dv, generator=torch.Generator(device="cuda").manual_seed(203), device="cuda").to(tdt[dt])
+    q = torch.zeros(B, H * dh, dtype=tdt[dt], device="cuda")
+    _sink(q, k, v, [at], gap, dh)
+    pos = torch.arange(L, device="cuda")
+    kv.k_pages[pages[pos // page], :, pos % page] = k.view(L, G, dh)
+    kv.v_pages[pages[pos // page], :, pos % page] = v.view(L, G, dv)
+    q, o = _decode(kv, dt, H, 0, 0, 204, scale=1.0, q=q)
+    _status_ok(hy, torch)
+    assert (o == o[0]).all()
+    want, a, big = ro.paged_attention(_np(q)[:1], _np(kv.k_pages), _np(kv.v_pages), kv.page_table.cpu().numpy(), [L], H,
+                                      0, 0, 1.0)
+    up = U["f16"] if dt == "f16" and gap > 20 else 2.0 ** -16
+    bound = _attn_bound(want, a, big, "f32", dh, dv, L, 1.0) + 2 * a * up + U[dt] * np.abs(want) + TINY[dt]
+    _hold(_np(o)[:1], want, bound, f"{dt} 2^-{gap}")
