@@ -285,10 +285,43 @@ struct Ring {
 };
 constexpr int blocks_per_sm(int dims, int ng) { return dims <= 192 && ng == 1 ? 3 : 2; }
 
+// One warp's sums of p v once more, key by key with fp32 weights, for values of V that are not finite:
+// the lower part of a weight may be 0, and 0 x infinity is NaN. m, l: [4][HB] of the block's warps;
+// acc: [HB][LD], brought to the block's max like the sums it replaces.
+template <typename T, int DH, int DV, int HB, int LD>
+__device__ __noinline__ void sums_again(const DecodeArgs<T>& a, const View w, int b, int g, int h0, int nh, int k0, int k1,
+                                        const float (*m)[HB], const float (*l)[HB], float* acc) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int h = 0; h < nh; ++h) {
+        const float mine = m[warp][h], mu = mine == -INFINITY ? 0.f : mine;
+        const float to = fmaxf(fmaxf(m[0][h], m[1][h]), fmaxf(m[2][h], m[3][h]));
+        const T* q = a.q + b * a.ldq + (long long)(h0 + h) * DH;
+        float sum[DV / 32] = {};
+        for (int j0 = k0 + warp * TK; j0 < k1; j0 += 4 * TK)
+            for (int j = j0; j < min(j0 + TK, k1); ++j) {
+                const long long slot = slot_of(a, b, w.pos(j));
+                if (slot < 0) continue;
+                const long long row = slot + (long long)g * a.page;
+                float s = 0.f;
+#pragma unroll
+                for (int e = lane; e < DH; e += 32) s = fmaf(to_f(q[e]), to_f(a.k_pages[row * DH + e]), s);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                const float p = fast_exp2(fmaf(s, a.scale_log2, -mu));
+#pragma unroll
+                for (int x = 0; x < DV / 32; ++x) sum[x] = fmaf(p, to_f(a.v_pages[row * DV + lane + 32 * x]), sum[x]);
+            }
+        float f = mine == -INFINITY ? 0.f : fast_exp2(mine - to);
+        if (!(l[warp][h] == l[warp][h])) f = l[warp][h];
+#pragma unroll
+        for (int x = 0; x < DV / 32; ++x) acc[h * LD + lane + 32 * x] = sum[x] * f;
+    }
+}
+
 // CL: the splits of one (KV head, sequence) form a thread-block cluster and join over distributed
 // shared memory; otherwise they leave partial results for the join kernel.
 template <typename T, int DH, int DV, int NG, bool CL>
-__global__ void __launch_bounds__(128, blocks_per_sm(DH + DV, NG)) decode_paged_mma_kernel(const DecodeArgs<T> a, int* status) {
+__global__ void __launch_bounds__(128, blocks_per_sm(DH + DV, NG)) decode_paged_mma_kernel(const __grid_constant__ DecodeArgs<T> a, int* status) {
     using R_ = Ring<DH, DV>;
     griddep_sync();
     extern __shared__ __align__(128) uint8_t decode_raw[];
@@ -470,8 +503,19 @@ __global__ void __launch_bounds__(128, blocks_per_sm(DH + DV, NG)) decode_paged_
     constexpr int LD = DV + 4;
     float* acc = reinterpret_cast<float*>(decode_raw);  // [4][8 NG][LD]
     static_assert(4 * 8 * NG * LD * 4 <= 4 * R_::SIZE, "the joined sums reuse the rings");
+    float odd = 0.f;  // NaN once a sum is not finite
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int t = 0; t < DV / 16; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) odd = fmaf(ot[n][t][e], 0.f, odd);
+    const bool again = __any_sync(0xffffffffu, !(odd == 0.f));
+    if (again)
+        sums_again<T, DH, DV, 8 * NG, LD>(a, w, b, g, h0, nh, k0, k1, ms, ls, acc + warp * 8 * NG * LD);
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
+        if (again) break;
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {

@@ -76,3 +76,35 @@ def test_decode_paged_long_tail_behind_a_sink(dt, gap, at):
     up = U["f16"] if dt == "f16" and gap > 20 else 2.0 ** -16
     bound = _attn_bound(want, a, big, "f32", dh, dv, L, 1.0) + 2 * a * up + U[dt] * np.abs(want) + TINY[dt]
     _hold(_np(o)[:1], want, bound, f"{dt} 2^-{gap}")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("inf", [float("inf"), float("-inf")])
+def test_decode_paged_infinite_values(dt, inf):
+    """A visible infinity in V makes its column infinite, whatever its weight (the lower part of a
+    weight in two parts may be 0), and nothing else: one key, many, several splits, a key with a small
+    weight, heads in two groups."""
+    torch, hy, rt, code, tdt = _mods()
+    for H, G, lens, page, window in ((4, 2, [1, 300, 40], 16, 0), (25, 5, [2500, 1, 700], 64, 0), (32, 1, [90, 1200, 33], 7, 200)):
+        kv = _cache(dt, lens, G, 64, 128, page, 205)
+        _, plain = _decode(kv, dt, H, 3, window, 206)
+        R = H // G
+        for b, pos, g, col in ((0, lens[0] - 1, 0, 5), (1, lens[1] // 2 if window == 0 else lens[1] - 100, G - 1, 127)):
+            if pos >= lens[b]:
+                continue
+            kv.v_pages[int(kv.page_table[b, pos // page]), g, pos % page, col] = inf
+        q, o = _decode(kv, dt, H, 3, window, 206)
+        _status_ok(hy, torch)
+        x, y = _np(o).reshape(3, H, 128), _np(plain).reshape(3, H, 128)
+        hit = np.zeros_like(x, dtype=bool)
+        hit[0, :R, 5] = True
+        hit[1, H - R:, 127] = True
+        assert (x[hit] == inf).all(), (H, G, x[hit])
+        lens_, want = np.array(lens), None
+        vp = kv.v_pages.clone()
+        vp[~torch.isfinite(vp)] = 0
+        want, a, big = ro.paged_attention(_np(q), _np(kv.k_pages), _np(vp), kv.page_table.cpu().numpy(), lens_, H, 3, window,
+                                          64 ** -0.5)
+        bound = _attn_bound(want, a, big, dt, 64, 128, max(lens), 64 ** -0.5)
+        keep = ~hit.reshape(3, -1)
+        _hold(_np(o)[keep], want[keep], bound[keep], f"{dt} {H} heads, other columns")
