@@ -217,8 +217,12 @@ attn_packed_simt_kernel(const T* __restrict__ q, long long ldq, const T* __restr
         float sum = l[r];
 #pragma unroll
         for (int w = 1; w < 16; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-        // (a NaN sum divides: a visible NaN reaches its row)
+        // (a NaN sum divides: a visible NaN reaches its row; without a score above -infinity the row is
+        // zero, whatever V holds)
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (sum == 0.f)
+#pragma unroll
+            for (int c = 0; c < DV / 32; ++c) acc[r][c] = make_float2(0.f, 0.f);
         if (i < L) {
             T* dst = o + (row0 + i) * ldo + (long long)h * DV + 4 * tx;
 #pragma unroll

@@ -21,7 +21,8 @@
 //               2^(s - m) as 16-bit pairs, the row sum of the fp32 values; O is rescaled in
 //               TMEM only when the running max grows by more than 2^4 (fp16) or 2^8 (bf16).
 // A CTA that noted a value that is not finite computes its rows once more from global
-// memory, key by key over what each row sees.
+// memory, key by key over what each row sees; so does a row whose sums are not finite (a visible
+// infinity times a weight that rounds to 0 in 16 bits).
 // P is rounded to the rows' type, as an MMA operand has to be: half a step relative to each
 // weight, the size of the output's own rounding. fp16 has little range: m is the running max less
 // 11, so that P lies between 2^11 and 2^15 at the largest weight and keeps all its bits down to
@@ -184,7 +185,7 @@ __device__ __noinline__ void recompute_row(const T* q, const T* k, long long ldk
             }
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[c0 + e] = from_f<T>(acc[e] * inv);
+        for (int e = 0; e < 16; ++e) o[c0 + e] = from_f<T>(inv == 0.f ? 0.f : acc[e] * inv);
     }
 }
 
@@ -519,8 +520,8 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         }
         if (ok && nt > 0 && __all_sync(0xffffffffu, tc::mbar_wait(&s.o_done[t], 0, abort, wlim))) {
             tc::tc_fence_after();
-            // no visible score above -infinity: zeros; a NaN sum divides, so that a visible NaN
-            // reaches its row
+            // no visible score above -infinity: zeros, whatever V holds; a NaN sum divides, so that a
+            // visible NaN reaches its row
             const float inv = l == 0.f ? 0.f : 1.f / l;
             T* orow = static_cast<T*>(a.o) + (it.start + (long long)i) * a.ldo + (long long)h * DV;
             // 64 columns at a time through the tile's Q (no longer needed): the warp's 32 rows there,
@@ -528,6 +529,7 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
             uint8_t* mid = s.q[t][0] + q * 4096;
             T* out = orow - (long long)lane * a.ldo;  // the warp's first row
             const int n = L - i + lane;               // rows from there to the sequence's end
+            float odd = 0.f;                          // NaN once a sum of the row is not finite
 #pragma unroll 1
             for (int v0 = 0; v0 < DV; v0 += 64) {
 #pragma unroll
@@ -535,6 +537,8 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                     uint32_t rr[32];
                     tc::tmem_ld32(o_cols + v0 + c * 32, rr);
                     tc::tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) odd = fmaf(__uint_as_float(rr[x]), 0.f, odd);
 #pragma unroll
                     for (int x = 0; x < 32; x += 8) {
                         uint4 pk;
@@ -554,7 +558,7 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 }
                 __syncwarp();
             }
-            if (i < L && *reinterpret_cast<volatile int*>(&s.dirty))
+            if (i < L && (!(odd == 0.f) || *reinterpret_cast<volatile int*>(&s.dirty)))
                 recompute_row<T, DH, DV>(static_cast<const T*>(a.q) + (it.start + (long long)i) * a.ldq + (long long)h * DH,
                                          static_cast<const T*>(a.k) + it.start * a.ldk + (long long)g * DH, a.ldk,
                                          static_cast<const T*>(a.v) + it.start * a.ldv + (long long)g * DV, a.ldv, orow, i,

@@ -108,3 +108,50 @@ def test_decode_paged_infinite_values(dt, inf):
         bound = _attn_bound(want, a, big, dt, 64, 128, max(lens), 64 ** -0.5)
         keep = ~hit.reshape(3, -1)
         _hold(_np(o)[keep], want[keep], bound[keep], f"{dt} {H} heads, other columns")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_packed_attention_infinite_values_of_small_weight(dt):
+    """An infinity in V makes its column of every row that sees it infinite, also where its weight is
+    far below what the rows' type can hold beside the largest (2^-60), also in key blocks that all
+    rows of a tile see."""
+    torch, hy, rt, code, tdt = _mods()
+    H, G, dh, dv, L, at = 2, 1, 64, 64, 900, 3
+    q, k, v, cu = _packed(dt, [L], H, G, dh, dv, 207, pad=0)
+    q[:, ::dh] = 8.0
+    k[:, 0] = 0.0
+    k[at, 0] = -60 * float(np.log(2.0)) / 8.0 * 8.0  # scale 1/8
+    k[at, 1:] = 0.0
+    v[at, 7] = float("inf")
+    o = torch.zeros(L, H * dv, dtype=tdt[dt], device="cuda")
+    rt.attn_prefill_packed(hy.attn_shape(H, G, dh, dv, 0, 0, code[dt]), q, k, v, cu, o)
+    _status_ok(hy, torch)
+    v2 = v.clone()
+    v2[at, 7] = 0.0
+    want, a, big = ro.packed_attention(_np(q), _np(k), _np(v2), [0, L], H, G, 0, 0, dh ** -0.5)
+    hit = np.zeros_like(want, dtype=bool)
+    hit[at:, 7::dv] = True
+    got = _np(o)
+    assert (got[hit] == np.inf).all(), f"{np.count_nonzero(got[hit] != np.inf)} of {hit.sum()}"
+    bound = _attn_bound(want, a, big, dt, dh, dv, L, dh ** -0.5)
+    _hold(got[~hit], want[~hit], bound[~hit], f"{dt} other columns")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_packed_attention_rows_without_a_score_are_zero(dt):
+    """Rows whose visible scores are all -infinity return zeros, whatever V holds."""
+    torch, hy, rt, code, tdt = _mods()
+    H, G, dh, dv, L = 2, 1, 64, 64, 300
+    q, k, v, cu = _packed(dt, [L], H, G, dh, dv, 208, pad=0)
+    none = torch.tensor([0, 5, 130, 299], device="cuda")
+    k[:, 3] = 1.0
+    q[none] = 0.0
+    q[none, 3] = float("-inf")
+    q[none, dh + 3] = float("-inf")
+    k[:, :3], k[:, 4:] = 0.5, 0.5
+    v[2, 9] = float("inf")
+    v[200, 11] = float("nan")
+    o = torch.full((L, H * dv), 7.0, dtype=tdt[dt], device="cuda")
+    rt.attn_prefill_packed(hy.attn_shape(H, G, dh, dv, 0, 0, code[dt]), q, k, v, cu, o)
+    _status_ok(hy, torch)
+    assert (o[none] == 0).all()
