@@ -162,18 +162,19 @@ __device__ __forceinline__ void make_tables(Tables& t, float g0, float g1, float
     // a decay below 2^-160 is 0 in fp32; the limit keeps -infinity out of the sums
     const double d0 = g0 < -1.0e2f ? fmax((double)g0 * LOG2E, -160.0) : (double)g0 * LOG2E;
     const double d1 = g1 < -1.0e2f ? fmax((double)g1 * LOG2E, -160.0) : (double)g1 * LOG2E;
-    double x1 = d0 + d1;
+    double sum = d0 + d1;
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, x1, w);
-        if (lane >= w) x1 += y;
+        const double y = __shfl_up_sync(0xffffffffu, sum, w);
+        if (lane >= w) sum += y;
     }
-    const double x0 = x1 - d1, last = __shfl_sync(0xffffffffu, x1, 31);
-    // (x1 - d1 loses nothing that matters: the sums stay below 2^14, their steps at 2^-39)
+    // forward from the rows before, so that a NaN or an infinity reaches no earlier row
+    const double last = __shfl_sync(0xffffffffu, sum, 31), before = __shfl_up_sync(0xffffffffu, sum, 1);
+    const double x0 = lane ? before + d0 : d0, x1 = x0 + d1;
     double from = 0.0;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-        const double c = b == 0 ? 0.0 : __shfl_sync(0xffffffffu, x1, b == 0 ? 0 : 8 * b - 1);
+        const double c = b == 0 ? 0.0 : __shfl_sync(0xffffffffu, sum, b == 0 ? 0 : 8 * b - 1);
         if ((lane >> 3) == b) from = c;
         if ((lane >> 3) <= b)
             *reinterpret_cast<float2*>(&t.b[b][2 * lane]) = make_float2((float)(c - x0), (float)(c - x1));

@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 
 from oracle import ragged_oracle as ro
-from test_gpu_ragged import TINY, U, _attn_bound, _cache, _decode, _hold, _mods, _np, _packed, _status_ok
+from test_gpu_ragged import (TINY, U, _attn_bound, _cache, _decode, _hold, _linear, _linear_bounds, _mods,
+                             _np, _offsets, _packed, _run_linear, _status_ok)
 
 pytestmark = pytest.mark.gpu
 
@@ -155,3 +156,33 @@ def test_packed_attention_rows_without_a_score_are_zero(dt):
     rt.attn_prefill_packed(hy.attn_shape(H, G, dh, dv, 0, 0, code[dt]), q, k, v, cu, o)
     _status_ok(hy, torch)
     assert (o[none] == 0).all()
+
+
+ALL_DIMS = [(16, 64), (64, 64), (64, 128), (128, 64)]
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dims", ALL_DIMS)
+@pytest.mark.parametrize("at", [0, 37, 38, 39, 40, 131])
+def test_linear_attention_decay_that_is_no_number(dt, dims, at):
+    """NaN or +infinity as one row's log decay: the rows before it and the other sequence keep their
+    values, the row and those behind it are not finite."""
+    torch, hy, rt, code, tdt = _mods()
+    lens, Hk, H, (dk, dv) = [180, 40], 1, 2, dims
+    x = _linear(dt, lens, Hk, H, dk, dv, 211)
+    q, k, v, g, st, cu = x
+    n = sum(lens)
+    want, oa, we, ea = ro.linear_attention(*(_np(t)[:n] for t in (q, k, v, g)), _offsets(lens), Hk, H, dk ** -0.5, _np(st))
+    ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
+    for bad in (float("nan"), float("inf")):
+        gg = g.clone()
+        gg[at] = bad
+        o, end = _run_linear(dt, x, Hk, H, dk, dv, True, g=gg)
+        _status_ok(hy, torch)
+        got, ge = _np(o)[:n], _np(end)
+        sees = np.zeros(n, dtype=bool)
+        sees[at:lens[0]] = True
+        _hold(got[~sees], want[~sees], ob[~sees], f"{dt} {dims} {bad} at {at}, rows that do not see it")
+        assert not np.isfinite(got[sees]).any()
+        assert not np.isfinite(ge[0]).any()
+        _hold(ge[1], we[1], eb[1], "the other state")
