@@ -24,7 +24,7 @@
 // which are taken out again from the fp32 sums.
 // A row's values reach only what sees them: rows behind the sequence are zero-filled; in a
 // chunk where a decay may underflow to 0, what it multiplies is dropped; a chunk whose V holds a
-// value that is not finite forms P V row by row.
+// value that is not finite forms P V, and one whose K or V does its state, row by row.
 // Bound: HBM (q, k, v once per 64 value columns, o) and the warp MMAs (1024 multiply-adds per
 // clock and SM measured) are close; what is left is instruction issue, hence the tables that
 // one warp (the one with the fewest tiles of P) forms a chunk ahead for all. Eight prompts of 2000
@@ -155,6 +155,33 @@ __device__ __noinline__ float row_product(const Tables& tab, const uint8_t* p, c
     return sum;
 }
 
+// The state after a chunk, row by row in fp32 over the rows it still sees: S is the warp's share, val its
+// first value column of the tile.
+template <typename T, int DK>
+__device__ __forceinline__ void row_states(const Tables& tab, const uint8_t* k, const uint8_t* v, int val, float (&S)[DK / 8][4]) {
+    const int lq = threadIdx.x & 3;
+#pragma unroll
+    for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[n][e] = fade(tab.dec, S[n][e]);
+#pragma unroll 1
+    for (int j = 0; j < CQ; ++j) {
+        const float w = tab.w[j];
+        if (w == 0.f) continue;
+        const float x = w * to_f(*reinterpret_cast<const T*>(v + at<CV>(j, val >> 3) + 2 * (val & 7)));
+        const float y = w * to_f(*reinterpret_cast<const T*>(v + at<CV>(j, (val >> 3) + 1) + 2 * (val & 7)));
+#pragma unroll
+        for (int n = 0; n < DK / 8; ++n) {
+            const uint32_t kk = *reinterpret_cast<const uint32_t*>(k + at<DK>(j, n) + 4 * lq);
+            const T* e = reinterpret_cast<const T*>(&kk);
+            S[n][0] = fmaf(x, to_f(e[0]), S[n][0]);
+            S[n][1] = fmaf(x, to_f(e[1]), S[n][1]);
+            S[n][2] = fmaf(y, to_f(e[0]), S[n][2]);
+            S[n][3] = fmaf(y, to_f(e[1]), S[n][3]);
+        }
+    }
+}
+
 // the tables of one chunk from the two log decays each lane holds (rows 2 lane, 2 lane + 1)
 __device__ __forceinline__ void make_tables(Tables& t, float g0, float g1, float log2_scale) {
     constexpr double LOG2E = 1.4426950408889634;
@@ -276,11 +303,14 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
             g0 = decay(t0 + 2 * CQ + 2 * lane);
             g1 = decay(t0 + 2 * CQ + 2 * lane + 1);
         }
-        // ---- P: rows 16 warp + lg (+8) ----
+        // ---- P: rows 16 warp + lg (+8). A row of K that is not finite shows in every score with it,
+        // so in the diagonal tiles ----
+        bool odd_k;
         {
             const float a0 = tab.a[16 * warp + lg], a1 = tab.a[16 * warp + lg + 8];
             float pr[4][2][4];
             float mx0 = 0.f, mx1 = 0.f;
+            float any = 0.f;  // NaN once a score of the diagonal tile is not finite
 #pragma unroll
             for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
@@ -305,6 +335,9 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
                     for (int n = 0; n < 2; ++n) {
                         const float2 bj = *reinterpret_cast<const float2*>(&tab.b[warp][16 * jt + 8 * n + 2 * lq]);
                         float* p = pr[jt][n];
+                        if (jt == warp)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) any = fmaf(p[e], 0.f, any);
                         const float w0 = fast_exp2(a0 + bj.x), w1 = fast_exp2(a0 + bj.y);
                         const float w2 = fast_exp2(a1 + bj.x), w3 = fast_exp2(a1 + bj.y);
                         if (!resets) {
@@ -332,6 +365,7 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
                     }
                 }
             }
+            odd_k = !(any == 0.f);
             float f0 = 1.f, f1 = 1.f;
             if (F16) {
 #pragma unroll
@@ -423,7 +457,7 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
             }
             odd = __any_sync(0xffffffffu, (bits(any) & 0x7fff7fffu) != 0);
         }
-        __syncthreads();  // P is there
+        odd_k = __syncthreads_or(odd_k);  // P is there; K of the whole chunk
         // ---- + P V ----
         if (!odd) {
             if (F16) {
@@ -471,7 +505,9 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
             orow = x;
         }
         // ---- state ----
-        {
+        if (odd || odd_k) {
+            row_states<T, DK>(tab, ks, vs, 16 * warp + lg, st);
+        } else {
             float fv = 1.f;
             if (F16) {
                 auto mx = __habs2(pair<T>(vf[0][0]));
@@ -507,13 +543,10 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const float2 w = *reinterpret_cast<const float2*>(&tab.w[16 * kk + 8 * x + 2 * lq]);
-                    uint32_t keep = 0xffffffffu;
-                    if (resets) keep = (w.x == 0.f ? 0u : 0x0000ffffu) | (w.y == 0.f ? 0u : 0xffff0000u);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         // V fragment (values 8 y .., rows 8 x ..) is operand part 2 x + y
-                        const uint32_t vv = resets ? vf[kk][2 * y + x] & keep : vf[kk][2 * y + x];
-                        const T* e = reinterpret_cast<const T*>(&vv);
+                        const T* e = reinterpret_cast<const T*>(&vf[kk][2 * y + x]);
                         const float2 z = __fmul2_rn(make_float2(to_f(e[0]), to_f(e[1])), w);
                         part[0][2 * x + y] = pack2<T>(z.x, z.y);
                         float2 left = z;

@@ -186,3 +186,37 @@ def test_linear_attention_decay_that_is_no_number(dt, dims, at):
         assert not np.isfinite(got[sees]).any()
         assert not np.isfinite(ge[0]).any()
         _hold(ge[1], we[1], eb[1], "the other state")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dims", ALL_DIMS)
+@pytest.mark.parametrize("at,reset", [(5, 9), (10, 200), (70, 71), (20, 100)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_linear_attention_rows_before_a_reset_are_forgotten(dt, dims, at, reset, bad):
+    """A key, value, query or start state that is not finite before a row that forgets everything:
+    rows before the one and from the other on, and the state, keep their values."""
+    torch, hy, rt, code, tdt = _mods()
+    lens, Hk, H, (dk, dv) = [260, 40], 1, 2, dims
+    x = _linear(dt, lens, Hk, H, dk, dv, 212, decay=0.05)
+    q, k, v, g, st, cu = x
+    n = sum(lens)
+    g[reset] = float("-inf")
+    want, oa, we, ea = ro.linear_attention(*(_np(t)[:n] for t in (q, k, v, g)), _offsets(lens), Hk, H, dk ** -0.5, _np(st))
+    ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
+    for what in "kvqs":
+        y = [t.clone() for t in (q, k, v)]
+        s2 = st.clone()
+        first = at
+        if what == "s":
+            s2[0, :, :, 1] = bad
+            first = 0
+        else:
+            y["qkv".index(what)][at] = bad
+        o, end = _run_linear(dt, (*y, g, s2, cu), Hk, H, dk, dv, True)
+        _status_ok(hy, torch)
+        got = _np(o)[:n]
+        sees = np.zeros(n, dtype=bool)
+        sees[first:at + 1 if what == "q" else reset] = True
+        _hold(got[~sees], want[~sees], ob[~sees], f"{dt} {dims} {what}={bad}, rows that do not see it")
+        assert not np.isfinite(got[sees]).any(), what
+        _hold(_np(end), we, eb, f"{dt} {dims} {what}={bad} states")
