@@ -33,8 +33,9 @@
 // Few long sequences are cut into segments of whole chunks (`segment_rows`): the same kernel first
 // forms what each segment adds to a state of zero, a small one turns these into the state before
 // each segment, and the segments then run side by side.
-// A CTA that noted a value of V that is not finite computes its rows once more by the
-// recurrence, in which nothing reaches a row that does not see it.
+// A CTA that noted a value of V, or of a row of K that the state takes up, that is not finite computes
+// its rows once more by the recurrence, in which nothing reaches a row that does not see it and an
+// infinity stays one (its parts would be infinity minus infinity).
 // Bound: HBM (q, k, v read and o written once per 128 value columns); what is left is the chain of a
 // chunk, about 6900 clocks, and the last sequences' chunks alone. Eight prompts of up to 4224 rows
 // (19800 in all), 25 heads of 64 x 128, bf16: 124 us, 49% of the copy rate.
@@ -237,10 +238,13 @@ __device__ __noinline__ void recurrence(const Args& a, const float* from, float*
 }
 
 // Row r of K' = w k as parts of T; w = 0 drops the row. The 16-byte pieces are swizzled by the row.
+// Returns whether the row holds a value that is not finite (bf16; of fp16's the largest is looked at).
 template <typename T, int PARTS>
-__device__ __forceinline__ void scaled_keys(uint8_t (*ks)[TILE], const uint8_t* krow, int r, float w) {
+__device__ __forceinline__ bool scaled_keys(uint8_t (*ks)[TILE], const uint8_t* krow, int r, float w) {
     const float2 w2 = make_float2(w, w);
     const bool drop = w == 0.f;
+    const __nv_bfloat162 nul = __floats2bfloat162_rn(0.f, 0.f);
+    __nv_bfloat162 odd = nul;  // 0 x (not finite) is NaN
 #pragma unroll 2
     for (int e = 0; e < 8; ++e) {
         const int at = (e ^ (r & 7)) * 16;
@@ -250,6 +254,8 @@ __device__ __forceinline__ void scaled_keys(uint8_t (*ks)[TILE], const uint8_t* 
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             float2 y = drop ? make_float2(0.f, 0.f) : __fmul2_rn(unpack2<T>(kw[x]), w2);
+            if constexpr (std::is_same<T, bf16>::value)
+                odd = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&kw[x]), nul, odd);
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
                 part[p][x] = pack2<T>(y.x, y.y);
@@ -263,6 +269,7 @@ __device__ __forceinline__ void scaled_keys(uint8_t (*ks)[TILE], const uint8_t* 
         for (int p = 0; p < PARTS; ++p)
             *reinterpret_cast<uint4*>(ks[p] + r * 128 + at) = make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
     }
+    return !drop && (*reinterpret_cast<const uint32_t*>(&odd) & 0x7fff7fffu) != 0;
 }
 
 // the power of two of a chunk's K' from its four warps' largest values
@@ -675,6 +682,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     }
                 }
                 m = fade(w, m);
+                if (m == INFINITY) *reinterpret_cast<volatile int*>(&s.dirty) = 1;
 #pragma unroll
                 for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
                 if (lane == 0) s.kmax[b][quad] = m;
@@ -734,7 +742,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             tc::fence_proxy_async_smem();
             tc::tc_fence_before();
             tc::mbar_arrive(&s.s_ready);
-            scaled_keys<T, PARTS>(s.ks, krow, r, w * fk);
+            if (scaled_keys<T, PARTS>(s.ks, krow, r, w * fk)) *reinterpret_cast<volatile int*>(&s.dirty) = 1;
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(&s.k_ready);
         }

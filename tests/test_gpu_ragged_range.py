@@ -220,3 +220,34 @@ def test_linear_attention_rows_before_a_reset_are_forgotten(dt, dims, at, reset,
         _hold(got[~sees], want[~sees], ob[~sees], f"{dt} {dims} {what}={bad}, rows that do not see it")
         assert not np.isfinite(got[sees]).any(), what
         _hold(_np(end), we, eb, f"{dt} {dims} {what}={bad} states")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dims", ALL_DIMS)
+def test_linear_attention_infinities_in_the_state(dt, dims):
+    """An infinite key element makes its column of the state infinite, an infinite value its row
+    (NaN only where it meets a 0), and the rest of the state stays."""
+    torch, hy, rt, code, tdt = _mods()
+    lens, Hk, H, (dk, dv), at = [200], 1, 2, dims, 90
+    x = _linear(dt, lens, Hk, H, dk, dv, 213, decay=0.05)
+    q, k, v, g, st, cu = x
+    for what in "kv":
+        y = [t.clone() for t in (q, k, v)]
+        if what == "k":
+            y[1][at, 7] = float("-inf")
+        else:
+            y[2][at, dv + 9] = float("inf")
+        o, end = _run_linear(dt, (*y, g, st, cu), Hk, H, dk, dv, True)
+        _status_ok(hy, torch)
+        with np.errstate(invalid="ignore"):
+            want, oa, we, ea = ro.linear_attention(*(_np(t)[:200] for t in (*y, g)), _offsets(lens), Hk, H, dk ** -0.5, _np(st))
+        got, fin = _np(end), np.isfinite(we)
+        assert np.count_nonzero(~fin) == (H * dv if what == "k" else dk)
+        ob, eb = _linear_bounds(np.where(fin, we, 0), np.where(fin, ea, 0), np.where(fin, we, 0), np.where(fin, ea, 0), dt,
+                                200, dk)
+        _hold(got[fin], we[fin], eb[fin], f"{dt} {dims} {what}: the rest of the state")
+        assert np.array_equal(got[~fin], we[~fin], equal_nan=True), f"{dt} {dims} {what}"
+        go, fo = _np(o)[:200], np.isfinite(want)
+        ob, _ = _linear_bounds(np.where(fo, want, 0), np.where(fo, oa, 0), we, ea, dt, 200, dk)
+        _hold(go[fo], want[fo], ob[fo], f"{dt} {dims} {what}: the rest of the rows")
+        assert not np.isfinite(go[~fo]).any()
