@@ -19,9 +19,10 @@
 // the fp32 distances of cs_i and cs_j from the cs at the start of i's 16 rows, so it is right
 // to fp32 after any other row (one that forgets everything included) and never formed from two
 // factors. P and the copy of S that meets q are rounded to the rows' type, like any MMA operand;
-// the scaled v of the state update enters as three parts (bf16) or two (fp16), so the fp32 state
-// keeps 22 bits or more of every term. fp16 has little range: P's rows, S's copy and v are brought to the middle of it by powers of two,
-// which are taken out again from the fp32 sums.
+// the scaled v of the state update enters as three parts (bf16: 24 bits) or two (fp16: 22 bits, or
+// 2^-37 of the column's largest scaled v in the chunk where that is more). fp16 has little range: P's
+// rows and each value column of S's copy and of the scaled v are brought to the middle of it by powers of
+// two, which are taken out again from the fp32 sums.
 // A row's values reach only what sees them: rows behind the sequence are zero-filled; in a
 // chunk where a decay may underflow to 0, what it multiplies is dropped; a chunk whose V holds a
 // value that is not finite forms P V, and one whose K or V does its state, row by row.
@@ -49,7 +50,6 @@ struct Tables {
     alignas(16) float w[CQ];      // 2^(cs_63 - cs_j)
     float dec;                    // 2^cs_63
     int resets;                   // a decay within the chunk may be 0
-    int grows;                    // a log decay is positive
 };
 
 template <int DK>
@@ -142,6 +142,18 @@ __device__ __forceinline__ void scale_rows(float (&x)[2][4], float a, float b) {
     }
 }
 
+// the two value rows of the warp's share of the state
+template <int N>
+__device__ __forceinline__ void scale_state(float (&st)[N][4], float a, float b) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        st[n][0] *= a;
+        st[n][1] *= a;
+        st[n][2] *= b;
+        st[n][3] *= b;
+    }
+}
+
 // sum_{j <= i} P_ij v_j of one value column, over the rows that i sees through a decay above 0
 template <typename T>
 __device__ __noinline__ float row_product(const Tables& tab, const uint8_t* p, const uint8_t* v, int i, int col) {
@@ -212,14 +224,12 @@ __device__ __forceinline__ void make_tables(Tables& t, float g0, float g1, float
         make_float2(fast_exp2((float)x0 + log2_scale), fast_exp2((float)x1 + log2_scale));
     *reinterpret_cast<float2*>(&t.w[2 * lane]) =
         make_float2(fast_exp2((float)(last - x0)), fast_exp2((float)(last - x1)));
-    const int grows = __any_sync(0xffffffffu, !(fmax(d0, d1) <= 0.0));
     float down = fminf((float)d0, 0.f) + fminf((float)d1, 0.f);
 #pragma unroll
     for (int w = 16; w; w >>= 1) down += __shfl_xor_sync(0xffffffffu, down, w);
     if (lane == 0) {
         t.dec = fast_exp2((float)last);
         t.resets = !(down + fminf(log2_scale, 0.f) > -120.f);
-        t.grows = grows;
     }
 }
 
@@ -373,8 +383,8 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
                     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, w));
                     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, w));
                 }
-                f0 = to_middle(mx0, -40, 40);
-                f1 = to_middle(mx1, -40, 40);
+                f0 = to_middle(mx0, -100, 100);
+                f1 = to_middle(mx1, -100, 100);
                 if (lq == 0) {
                     sm.ps[16 * warp + lg] = f0;
                     sm.ps[16 * warp + lg + 8] = f1;
@@ -400,22 +410,26 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
 #pragma unroll
             for (int e = 0; e < 4; ++e) out[mt][0][e] = out[mt][1][e] = 0.f;
         if (c > 0 || state_in) {
-            float fs = 1.f;
+            // fp16: each value column's power of two
+            float fs[2] = {1.f, 1.f};
             if (F16) {
-                float mx = 0.f;
+                float mx[2] = {0.f, 0.f};
 #pragma unroll
                 for (int n = 0; n < NKT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(st[n][e]));
+                    for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], fabsf(st[n][e]));
 #pragma unroll
-                for (int w = 1; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-                fs = to_middle(mx, -100, 100);
+                for (int y = 0; y < 2; ++y) {
+                    mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], 1));
+                    mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], 2));
+                    fs[y] = to_middle(mx[y], -100, 100);
+                }
             }
-            auto part = [&](float x, float y) { return F16 ? pack2<T>(x * fs, y * fs) : pack2<T>(x, y); };
+            auto part = [&](float x, float y, int row) { return F16 ? pack2<T>(x * fs[row], y * fs[row]) : pack2<T>(x, y); };
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
-                const uint32_t b0 = part(st[2 * kk][0], st[2 * kk][1]), b1 = part(st[2 * kk + 1][0], st[2 * kk + 1][1]);
-                const uint32_t b2 = part(st[2 * kk][2], st[2 * kk][3]), b3 = part(st[2 * kk + 1][2], st[2 * kk + 1][3]);
+                const uint32_t b0 = part(st[2 * kk][0], st[2 * kk][1], 0), b1 = part(st[2 * kk + 1][0], st[2 * kk + 1][1], 0);
+                const uint32_t b2 = part(st[2 * kk][2], st[2 * kk][3], 1), b3 = part(st[2 * kk + 1][2], st[2 * kk + 1][3], 1);
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
                     uint32_t qf[4];
@@ -424,10 +438,24 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
                     wm::mma16<T>(out[mt][1], qf, b2, b3);
                 }
             }
-            const float back = F16 ? 1.f / fs : 1.f;
+            if (F16) {
+                // this lane's columns 2 lq and 2 lq + 1 of both halves lie in the lanes with that lg
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float back = inverse(fs[n]);
+                    const float b0 = __shfl_sync(0xffffffffu, back, 8 * lq), b1 = __shfl_sync(0xffffffffu, back, 8 * lq + 4);
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt) {
+                        out[mt][n][0] *= b0;
+                        out[mt][n][1] *= b1;
+                        out[mt][n][2] *= b0;
+                        out[mt][n][3] *= b1;
+                    }
+                }
+            }
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                const float ea = tab.e[16 * mt + lg] * back, eb = tab.e[16 * mt + lg + 8] * back;
+                const float ea = tab.e[16 * mt + lg], eb = tab.e[16 * mt + lg + 8];
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     if (!resets) {
@@ -508,31 +536,40 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
         if (odd || odd_k) {
             row_states<T, DK>(tab, ks, vs, 16 * warp + lg, st);
         } else {
-            float fv = 1.f;
+            // fp16: each value column's power of two, from its largest weighted value
+            float fv[2] = {1.f, 1.f};
             if (F16) {
-                auto mx = __habs2(pair<T>(vf[0][0]));
+                float m[2] = {0.f, 0.f};
 #pragma unroll
-                for (int x = 1; x < 16; ++x) mx = __hmax2(mx, __habs2(pair<T>(vf[x >> 2][x & 3])));
-                float m = fmaxf(__low2float(mx), __high2float(mx));
+                for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-                for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-                // (never down, where it would cost small values their last bits, unless a weight is above 1)
-                fv = to_middle(m, tab.grows ? -15 : 0, 15);
-                const auto f2 = pair<T>(pack2<T>(fv, fv));
+                    for (int x = 0; x < 2; ++x) {
+                        const float2 w = *reinterpret_cast<const float2*>(&tab.w[16 * kk + 8 * x + 2 * lq]);
 #pragma unroll
-                for (int x = 0; x < 16; ++x) vf[x >> 2][x & 3] = bits(__hmul2(pair<T>(vf[x >> 2][x & 3]), f2));
+                        for (int y = 0; y < 2; ++y) {
+                            const T* e = reinterpret_cast<const T*>(&vf[kk][2 * y + x]);
+                            const float2 z = __fmul2_rn(make_float2(to_f(e[0]), to_f(e[1])), w);
+                            m[y] = fmaxf(m[y], fmaxf(fabsf(z.x), fabsf(z.y)));
+                        }
+                    }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    m[y] = fmaxf(m[y], __shfl_xor_sync(0xffffffffu, m[y], 1));
+                    m[y] = fmaxf(m[y], __shfl_xor_sync(0xffffffffu, m[y], 2));
+                    fv[y] = to_middle(m[y], -100, 40);
+                }
             }
-            const float dec = tab.dec * fv;
+            const float dec0 = tab.dec * fv[0], dec1 = tab.dec * fv[1];
             if (!resets) {
-#pragma unroll
-                for (int n = 0; n < NKT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) st[n][e] *= dec;
+                scale_state<NKT>(st, dec0, dec1);
             } else {
 #pragma unroll
-                for (int n = 0; n < NKT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) st[n][e] = fade(dec, st[n][e]);
+                for (int n = 0; n < NKT; ++n) {
+                    st[n][0] = fade(dec0, st[n][0]);
+                    st[n][1] = fade(dec0, st[n][1]);
+                    st[n][2] = fade(dec1, st[n][2]);
+                    st[n][3] = fade(dec1, st[n][3]);
+                }
             }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
@@ -547,7 +584,8 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
                     for (int y = 0; y < 2; ++y) {
                         // V fragment (values 8 y .., rows 8 x ..) is operand part 2 x + y
                         const T* e = reinterpret_cast<const T*>(&vf[kk][2 * y + x]);
-                        const float2 z = __fmul2_rn(make_float2(to_f(e[0]), to_f(e[1])), w);
+                        const float2 wf = F16 ? make_float2(w.x * fv[y], w.y * fv[y]) : w;
+                        const float2 z = __fmul2_rn(make_float2(to_f(e[0]), to_f(e[1])), wf);
                         part[0][2 * x + y] = pack2<T>(z.x, z.y);
                         float2 left = z;
 #pragma unroll
@@ -566,13 +604,7 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
                         wm::mma16<T>(st[2 * n + 1], part[p], kf[n][2], kf[n][3]);
                     }
             }
-            if (F16) {
-                const float back = inverse(fv);
-#pragma unroll
-                for (int n = 0; n < NKT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) st[n][e] *= back;
-            }
+            if (F16) scale_state<NKT>(st, inverse(fv[0]), inverse(fv[1]));
         }
     }
     wm::cpa_wait0();

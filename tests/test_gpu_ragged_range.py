@@ -251,3 +251,51 @@ def test_linear_attention_infinities_in_the_state(dt, dims):
         ob, _ = _linear_bounds(np.where(fo, want, 0), np.where(fo, oa, 0), we, ea, dt, 200, dk)
         _hold(go[fo], want[fo], ob[fo], f"{dt} {dims} {what}: the rest of the rows")
         assert not np.isfinite(go[~fo]).any()
+
+
+def _growth(dt, dims, grow):
+    """Positive log decays: the state grows by e^(grow x rows); the output's scale brings the last
+    rows back near 1."""
+    torch, hy, rt, code, tdt = _mods()
+    lens, Hk, H, (dk, dv) = [150, 33], 1, 2, dims
+    x = _linear(dt, lens, Hk, H, dk, dv, 214)
+    q, k, v, g, st, cu = x
+    g.copy_(grow * (0.5 + torch.rand(g.shape, generator=torch.Generator(device="cuda").manual_seed(215), device="cuda")))
+    scale = float(np.exp(-150 * grow)) * dk ** -0.5
+    o, end = _run_linear(dt, x, Hk, H, dk, dv, True, scale=scale)
+    _status_ok(hy, torch)
+    n = sum(lens)
+    want, oa, we, ea = ro.linear_attention(*(_np(t)[:n] for t in (q, k, v, g)), _offsets(lens), Hk, H, scale, _np(st))
+    ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
+    _hold(_np(o)[:n], want[:n], ob[:n], f"{dt} {dims} o")
+    _hold(_np(end), we, eb, f"{dt} {dims} state", 2.0 ** -16)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dims", [(16, 64), (128, 64)])
+@pytest.mark.parametrize("grow", [0.04, 0.1, 0.3, 0.45])
+def test_linear_attention_growth(dt, dims, grow):
+    _growth(dt, dims, grow)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(16, 64), (128, 64)])
+def test_linear_attention_value_columns_of_different_size(dt, dk, dv):
+    """Value columns near 2^13 beside ones near 2^-13, decays of 2^-8 over a chunk: each column of the state
+    keeps its own bits."""
+    torch, hy, rt, code, tdt = _mods()
+    lens, Hk, H = [150, 70], 1, 2
+    x = _linear(dt, lens, Hk, H, dk, dv, 216, decay=0.17)
+    q, k, v, g, st, cu = x
+    v[:, ::2] *= 2.0 ** 11
+    v[:, 1::2] *= 2.0 ** -13
+    st[..., ::2, :] *= 2.0 ** 11
+    st[..., 1::2, :] *= 2.0 ** -13
+    scale = 2.0 ** -4
+    o, end = _run_linear(dt, x, Hk, H, dk, dv, True, scale=scale)
+    _status_ok(hy, torch)
+    n = sum(lens)
+    want, oa, we, ea = ro.linear_attention(*(_np(t)[:n] for t in (q, k, v, g)), _offsets(lens), Hk, H, scale, _np(st))
+    ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
+    _hold(_np(o)[:n], want[:n], ob[:n], f"{dt} {dk} o")
+    _hold(_np(end), we, eb, f"{dt} {dk} state", 2.0 ** -16)
