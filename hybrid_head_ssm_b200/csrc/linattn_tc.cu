@@ -25,9 +25,9 @@
 // Numbers: a decay between rows of different 32-row blocks is A_i B_j, both distances from
 // the start of i's block and so at most 1 each (a chunk with a positive log decay forms
 // 2^(a_i + b_j) instead), within a block 2^(a_i + b_j); either way right to fp32 after any other
-// row (one that forgets everything included). K' enters as three parts (bf16) or two
-// (fp16), at least 22 bits of every term of the fp32 state; P and the state's copy are rounded
-// to the rows' type, like any MMA operand. fp16 has little range: P's rows, the copy's rows and
+// row (one that forgets everything included). K' enters as three parts (bf16: 24 bits) or two
+// (fp16: 22 bits, or 2^-37 of the chunk's largest weighted key where that is more); P and the state's
+// copy are rounded to the rows' type, like any MMA operand. fp16 has little range: P's rows, the copy's rows and
 // K' are brought to the middle of it by powers of two that the fp32 values give back (the
 // state in TMEM carries K's power, changed together with its decay).
 // Few long sequences are cut into segments of whole chunks (`segment_rows`): the same kernel first
@@ -272,9 +272,10 @@ __device__ __forceinline__ bool scaled_keys(uint8_t (*ks)[TILE], const uint8_t* 
     return !drop && (*reinterpret_cast<const uint32_t*>(&odd) & 0x7fff7fffu) != 0;
 }
 
-// the power of two of a chunk's K' from its four warps' largest values
+// the power of two of a chunk's K' from its four warps' largest values. Down as far as weights above 1
+// may need it; up as far as a state that is much larger than the chunk's keys leaves room in fp32
 __device__ __forceinline__ float k_power(const float* m) {
-    return to_middle(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), -15, 24);
+    return to_middle(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), -100, 24);
 }
 
 // 32 lanes x 32 columns of fp32, read
@@ -599,7 +600,7 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     for (int j = 0; j < 32; j += 2)
                         mx = fmax3(mx, j <= last ? fabsf(x[j]) : 0.f, j + 1 <= last ? fabsf(x[j + 1]) : 0.f);
                 }
-                f = to_middle(grows ? mx : mx * fast_exp2(a.log2_scale), -40, 40);
+                f = to_middle(grows ? mx : mx * fast_exp2(a.log2_scale), -100, 100);
                 s.ps[b][i] = f;
             }
             // P over the scores: block u goes to columns 16 u .. 16 u + 15, all read by then

@@ -299,3 +299,10 @@ def test_linear_attention_value_columns_of_different_size(dt, dk, dv):
     ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
     _hold(_np(o)[:n], want[:n], ob[:n], f"{dt} {dk} o")
     _hold(_np(end), we, eb, f"{dt} {dk} state", 2.0 ** -16)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dv", [64, 128])
+@pytest.mark.parametrize("grow", [0.04, 0.1, 0.3, 0.45])
+def test_linear_attention_growth_key_dim_64(dt, dv, grow):
+    _growth(dt, (64, dv), grow)
