@@ -16,9 +16,11 @@
 // serve as the B operand of P V and as the A operand of the update.
 //
 // Numbers: cs is summed in 64 bits. A decay between rows j <= i is 2^(a_i + b_j) with a_i and b_j
-// the fp32 distances of cs_i and cs_j from the cs at the start of i's 16 rows, so it is right
-// to fp32 after any other row (one that forgets everything included) and never formed from two
-// factors. P and the copy of S that meets q are rounded to the rows' type, like any MMA operand;
+// the fp32 distances of cs_i and cs_j from the cs at the start of i's 16 rows, and never formed from two
+// factors. A row that forgets everything (a decay that is 0 in fp32) is no term of cs but a border that
+// nothing before it passes, so the distances stay small after any number of them (only decays of 2^-100
+// and less that are not 0, row after row, leave the others of their 16 rows right to 2^-12, half a step of
+// P). P and the copy of S that meets q are rounded to the rows' type, like any MMA operand;
 // the scaled v of the state update enters as three parts (bf16: 24 bits) or two (fp16: 22 bits, or
 // 2^-37 of the column's largest scaled v in the chunk where that is more). fp16 has little range: P's
 // rows and each value column of S's copy and of the scaled v are brought to the middle of it by powers of
@@ -48,6 +50,7 @@ struct Tables {
     alignas(16) float b[4][CQ];   // cs at the start of 16-row block t - cs_j, for j < 16 (t + 1)
     alignas(16) float e[CQ];      // 2^cs_i scale
     alignas(16) float w[CQ];      // 2^(cs_63 - cs_j)
+    alignas(8) int border[CQ];    // the last row at or before each that forgets everything (below 0: none)
     float dec;                    // 2^cs_63
     int resets;                   // a decay within the chunk may be 0
 };
@@ -158,7 +161,7 @@ __device__ __forceinline__ void scale_state(float (&st)[N][4], float a, float b)
 template <typename T>
 __device__ __noinline__ float row_product(const Tables& tab, const uint8_t* p, const uint8_t* v, int i, int col) {
     float sum = 0.f;
-    for (int j = 0; j <= i; ++j) {
+    for (int j = max(tab.border[i], 0); j <= i; ++j) {
         if (fast_exp2(tab.a[i] + tab.b[i >> 4][j]) == 0.f) continue;
         const T pj = *reinterpret_cast<const T*>(p + at<CQ>(i, j >> 3) + 2 * (j & 7));
         const T vj = *reinterpret_cast<const T*>(v + at<CV>(j, col >> 3) + 2 * (col & 7));
@@ -198,9 +201,10 @@ __device__ __forceinline__ void row_states(const Tables& tab, const uint8_t* k, 
 __device__ __forceinline__ void make_tables(Tables& t, float g0, float g1, float log2_scale) {
     constexpr double LOG2E = 1.4426950408889634;
     const int lane = threadIdx.x & 31;
-    // a decay below 2^-160 is 0 in fp32; the limit keeps -infinity out of the sums
-    const double d0 = g0 < -1.0e2f ? fmax((double)g0 * LOG2E, -160.0) : (double)g0 * LOG2E;
-    const double d1 = g1 < -1.0e2f ? fmax((double)g1 * LOG2E, -160.0) : (double)g1 * LOG2E;
+    // below 2^-150 a decay is 0 in fp32
+    const bool r0 = g0 < -104.f, r1 = g1 < -104.f;
+    const unsigned m0 = __ballot_sync(0xffffffffu, r0), m1 = __ballot_sync(0xffffffffu, r1);
+    const double d0 = (double)(r0 ? 0.f : g0) * LOG2E, d1 = (double)(r1 ? 0.f : g1) * LOG2E;
     double sum = d0 + d1;
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
@@ -210,6 +214,19 @@ __device__ __forceinline__ void make_tables(Tables& t, float g0, float g1, float
     // forward from the rows before, so that a NaN or an infinity reaches no earlier row
     const double last = __shfl_sync(0xffffffffu, sum, 31), before = __shfl_up_sync(0xffffffffu, sum, 1);
     const double x0 = lane ? before + d0 : d0, x1 = x0 + d1;
+    // the last row that forgets everything at or before rows 2 lane and 2 lane + 1, and in the chunk
+    int f0 = -1, f1 = -1, border = -1;
+    if (m0 | m1) {
+        const unsigned below = (1u << lane) - 1;
+        auto row = [](unsigned even, unsigned odd) { return max(62 - 2 * __clz(even), 63 - 2 * __clz(odd)); };
+        f0 = row(m0 & (below | 1u << lane), m1 & below);
+        f1 = r1 ? 2 * lane + 1 : f0;
+        border = row(m0, m1);
+    }
+    float down = fminf((float)d0, 0.f) + fminf((float)d1, 0.f);
+#pragma unroll
+    for (int w = 16; w; w >>= 1) down += __shfl_xor_sync(0xffffffffu, down, w);
+    const bool resets = border >= 0 || !(down + fminf(log2_scale, 0.f) > -120.f);
     double from = 0.0;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -220,16 +237,14 @@ __device__ __forceinline__ void make_tables(Tables& t, float g0, float g1, float
     }
     *reinterpret_cast<float2*>(&t.a[2 * lane]) =
         make_float2((float)(x0 - from) + log2_scale, (float)(x1 - from) + log2_scale);
-    *reinterpret_cast<float2*>(&t.e[2 * lane]) =
-        make_float2(fast_exp2((float)x0 + log2_scale), fast_exp2((float)x1 + log2_scale));
-    *reinterpret_cast<float2*>(&t.w[2 * lane]) =
-        make_float2(fast_exp2((float)(last - x0)), fast_exp2((float)(last - x1)));
-    float down = fminf((float)d0, 0.f) + fminf((float)d1, 0.f);
-#pragma unroll
-    for (int w = 16; w; w >>= 1) down += __shfl_xor_sync(0xffffffffu, down, w);
+    *reinterpret_cast<int2*>(&t.border[2 * lane]) = make_int2(f0, f1);
+    *reinterpret_cast<float2*>(&t.e[2 * lane]) = make_float2(f0 >= 0 ? 0.f : fast_exp2((float)x0 + log2_scale),
+                                                             f1 >= 0 ? 0.f : fast_exp2((float)x1 + log2_scale));
+    *reinterpret_cast<float2*>(&t.w[2 * lane]) = make_float2(2 * lane < border ? 0.f : fast_exp2((float)(last - x0)),
+                                                             2 * lane + 1 < border ? 0.f : fast_exp2((float)(last - x1)));
     if (lane == 0) {
-        t.dec = fast_exp2((float)last);
-        t.resets = !(down + fminf(log2_scale, 0.f) > -120.f);
+        t.dec = border >= 0 ? 0.f : fast_exp2((float)last);
+        t.resets = resets;
     }
 }
 
@@ -356,10 +371,12 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
                             p[2] *= w2;
                             p[3] *= w3;
                         } else {
-                            p[0] = fade(w0, p[0]);
-                            p[1] = fade(w1, p[1]);
-                            p[2] = fade(w2, p[2]);
-                            p[3] = fade(w3, p[3]);
+                            const int j = 16 * jt + 8 * n + 2 * lq;
+                            const int from0 = tab.border[16 * warp + lg], from1 = tab.border[16 * warp + lg + 8];
+                            p[0] = j < from0 ? 0.f : fade(w0, p[0]);
+                            p[1] = j + 1 < from0 ? 0.f : fade(w1, p[1]);
+                            p[2] = j < from1 ? 0.f : fade(w2, p[2]);
+                            p[3] = j + 1 < from1 ? 0.f : fade(w3, p[3]);
                         }
                         if (jt == warp) {
                             const int j = 8 * n + 2 * lq;

@@ -306,3 +306,43 @@ def test_linear_attention_value_columns_of_different_size(dt, dk, dv):
 @pytest.mark.parametrize("grow", [0.04, 0.1, 0.3, 0.45])
 def test_linear_attention_growth_key_dim_64(dt, dv, grow):
     _growth(dt, (64, dv), grow)
+
+
+def _reset_and_growth(dt, dims):
+    """Rows that forget everything, then growth by e^40 and more within the same chunk: what lay
+    before them, a NaN among it, does not come back."""
+    torch, hy, rt, code, tdt = _mods()
+    lens, Hk, H, (dk, dv), at, reset = [60, 130], 1, 2, dims, 3, 6
+    x = _linear(dt, lens, Hk, H, dk, dv, 217)
+    q, k, v, g, st, cu = x
+    n = sum(lens)
+    g.fill_(0.8)
+    g[60:].fill_(0.4)
+    for r in (reset, 60 + reset, 60 + reset + 5):
+        g[r] = float("-inf")
+    scale = float(np.exp(-40.0)) * dk ** -0.5
+    want, oa, we, ea = ro.linear_attention(*(_np(t)[:n] for t in (q, k, v, g)), _offsets(lens), Hk, H, scale, _np(st))
+    ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
+    for what in "kvs":
+        y = [t.clone() for t in (q, k, v)]
+        s2 = st.clone()
+        if what == "s":
+            s2.fill_(float("nan"))
+        else:
+            for a in (at, 60 + at):
+                y["qkv".index(what)][a] = float("nan")
+        o, end = _run_linear(dt, (*y, g, s2, cu), Hk, H, dk, dv, True, scale=scale)
+        _status_ok(hy, torch)
+        got = _np(o)[:n]
+        sees = np.zeros(n, dtype=bool)
+        first = 0 if what == "s" else at
+        sees[first:reset] = sees[60 + first:60 + reset] = True
+        _hold(got[~sees], want[~sees], ob[~sees], f"{dt} {dims} {what}, rows that do not see it")
+        assert not np.isfinite(got[sees]).any()
+        _hold(_np(end), we, eb, f"{dt} {dims} {what} states")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dims", [(16, 64), (128, 64)])
+def test_linear_attention_growth_does_not_undo_a_reset(dt, dims):
+    _reset_and_growth(dt, dims)
