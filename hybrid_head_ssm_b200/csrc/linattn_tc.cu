@@ -24,8 +24,10 @@
 // chunk (unrolled, 3.8 of every 5 stalls were waits for instructions and a chunk took twice as long).
 // Numbers: a decay between rows of different 32-row blocks is A_i B_j, both distances from
 // the start of i's block and so at most 1 each (a chunk with a positive log decay forms
-// 2^(a_i + b_j) instead), within a block 2^(a_i + b_j); either way right to fp32 after any other
-// row (one that forgets everything included). K' enters as three parts (bf16: 24 bits) or two
+// 2^(a_i + b_j) instead), within a block 2^(a_i + b_j). A row that forgets everything (a decay that is 0
+// in fp32) is no term of cs but a border that nothing before it passes, so the distances stay small after
+// any number of them (only decays of 2^-100 and less that are not 0, row after row, leave the others of
+// their block right to 2^-11, a step of P). K' enters as three parts (bf16: 24 bits) or two
 // (fp16: 22 bits, or 2^-37 of the chunk's largest weighted key where that is more); P and the state's
 // copy are rounded to the rows' type, like any MMA operand. fp16 has little range: P's rows, the copy's rows and
 // K' are brought to the middle of it by powers of two that the fp32 values give back (the
@@ -61,7 +63,9 @@ constexpr uint32_t TM_S1 = 0, TM_O = 128, TM_O2 = 256, TM_D = 384;
 struct Tables {
     alignas(16) float a[CQ];       // cs_i - cs at the start of i's 32-row block + log2 scale
     alignas(16) float b[CQ];       // cs at the start of j's block - cs_j
-    alignas(16) float B[3][96];    // 2^(cs at the start of block t + 1 - cs_j), j below that block
+    // 2^(cs at the start of block t + 1 - cs_j), j below that block; in a chunk that resets or grows, from
+    // B[0][0] on, the last row at or before each that forgets everything (-1: none)
+    alignas(16) float B[3][96];
     alignas(16) float e[CQ];       // 2^cs_i scale
     alignas(16) float w[CQ];       // 2^(cs_127 - cs_j); 0 behind the sequence
     float between[4][4];           // cs at the start of block t - cs at the start of block u
@@ -134,7 +138,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
 // A lane's part of the tables of one chunk, from the log decays of rows 4 l .. 4 l + 3; n rows
 // are real.
 struct LaneTables {
-    float a[4], b[4], e[4], w[4], B[3][4], between, dec;
+    float a[4], b[4], e[4], w[4], B[3][4], border[4], between, dec;
     double total;  // the chunk's log2 decay
     int resets, grows;
     __device__ __forceinline__ void make(const float (&g)[4], int n, float lsc) {
@@ -143,13 +147,15 @@ struct LaneTables {
         double d[4];
         float down = 0.f;
         bool up = false;
+        unsigned m[4];  // the lanes whose i-th row forgets everything: below 2^-150 a decay is 0 in fp32
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            d[i] = (double)g[i] * LOG2E;
-            // a decay below 2^-160 is 0 in fp32; the limit keeps -infinity out of the sums
-            if (d[i] < -160.0) d[i] = -160.0;
-            down += fminf(g[i], 0.f);
-            up |= !(g[i] <= 0.f);
+            const bool r = g[i] < -104.f;
+            m[i] = __ballot_sync(0xffffffffu, r);
+            const float x = r ? 0.f : g[i];
+            d[i] = (double)x * LOG2E;
+            down += fminf(x, 0.f);
+            up |= !(x <= 0.f);
         }
         const double own = (d[0] + d[1]) + (d[2] + d[3]);
         double sum = own;
@@ -164,6 +170,10 @@ struct LaneTables {
         const double from = blk == 0 ? 0.0 : blk == 1 ? c1 : blk == 2 ? c2 : c3;
         double before = __shfl_up_sync(0xffffffffu, sum, 1);
         if (lane == 0) before = 0.0;
+        grows = __any_sync(0xffffffffu, up);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) down += __shfl_xor_sync(0xffffffffu, down, o);
+        resets = !(down * 1.4426950f + fminf(lsc, 0.f) > -120.f);
         double x = before;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -180,12 +190,28 @@ struct LaneTables {
         const double cr = r == 0 ? 0.0 : r == 1 ? c1 : r == 2 ? c2 : c3;
         const double cu = u == 0 ? 0.0 : u == 1 ? c1 : u == 2 ? c2 : c3;
         between = (float)(cr - cu);
-        grows = __any_sync(0xffffffffu, up);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) down += __shfl_xor_sync(0xffffffffu, down, o);
         total = last;
         dec = fast_exp2((float)last);
-        resets = !(down * 1.4426950f + fminf(lsc, 0.f) > -120.f);
+        border[0] = border[1] = border[2] = border[3] = -1.f;
+        if (m[0] | m[1] | m[2] | m[3]) {
+            const unsigned below = (1u << lane) - 1;
+            int at = -1, end = -1;  // of the rows before the lane's, and of the chunk
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                at = max(at, 4 * (31 - __clz(m[i] & below)) + i);
+                end = max(end, 4 * (31 - __clz(m[i])) + i);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (m[i] >> lane & 1) at = 4 * lane + i;
+                border[i] = (float)at;
+                if (at >= 0) e[i] = 0.f;
+                if (4 * lane + i < end) w[i] = 0.f;
+            }
+            total = -INFINITY;
+            dec = 0.f;
+            resets = 1;
+        }
     }
     __device__ __forceinline__ void store(Tables& t) const {
         const int lane = threadIdx.x & 31, blk = lane >> 3;
@@ -194,9 +220,13 @@ struct LaneTables {
         put(&t.b[4 * lane], b);
         put(&t.e[4 * lane], e);
         put(&t.w[4 * lane], w);
+        if (grows || resets) {
+            put(&t.B[0][0] + 4 * lane, border);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (blk <= i) put(&t.B[i][4 * lane], B[i]);
+            for (int i = 0; i < 3; ++i)
+                if (blk <= i) put(&t.B[i][4 * lane], B[i]);
+        }
         if (lane < 16) t.between[lane >> 2][lane & 3] = between;
         if (lane == 0) {
             t.dec = dec;
@@ -565,11 +595,13 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 } else {
                     const float base = ai + tab.between[blk][u];
                     const float2 base2 = make_float2(base, base);
-                    const int last = u < blk ? 31 : lane;
+                    unsigned see = u < blk ? 0xffffffffu : 0xffffffffu >> (31 - lane);
                     if (!plain) {
                         // a decay of 0 drops what it multiplies, also what is not finite
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = fast_exp2(base + tab.b[32 * u + j]) == 0.f ? 0.f : x[j];
+                        const int first = (int)(&tab.B[0][0])[i] - 32 * u;
+#pragma unroll 1
+                        for (int j = 0; j < 32; ++j)
+                            if (j < first || fast_exp2(base + tab.b[32 * u + j]) == 0.f) see &= ~(1u << j);
                     }
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
@@ -577,30 +609,30 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         const float2 d = __fadd2_rn(base2, make_float2(bj.x, bj.y)), e = __fadd2_rn(base2, make_float2(bj.z, bj.w));
                         const float2 y = __fmul2_rn(make_float2(fast_exp2(d.x), fast_exp2(d.y)), make_float2(x[j], x[j + 1]));
                         const float2 z = __fmul2_rn(make_float2(fast_exp2(e.x), fast_exp2(e.y)), make_float2(x[j + 2], x[j + 3]));
-                        x[j] = j <= last ? y.x : 0.f;
-                        x[j + 1] = j + 1 <= last ? y.y : 0.f;
-                        x[j + 2] = j + 2 <= last ? z.x : 0.f;
-                        x[j + 3] = j + 3 <= last ? z.y : 0.f;
+                        x[j] = see >> j & 1 ? y.x : 0.f;
+                        x[j + 1] = see >> (j + 1) & 1 ? y.y : 0.f;
+                        x[j + 2] = see >> (j + 2) & 1 ? z.x : 0.f;
+                        x[j + 3] = see >> (j + 3) & 1 ? z.y : 0.f;
                     }
                 }
             };
             float f = 1.f;
             if (F16) {
-                // the row's power of two, from its largest score (which bounds P unless a decay
-                // is above 1; then from P itself)
+                // the row's power of two, from its largest score, which bounds P; from P itself where a
+                // decay may be above 1 or hide a score
                 float mx = 0.f;
 #pragma unroll 1
                 for (int u = 0; u <= blk; ++u) {
                     float x[32];
                     ld32(s1 + 32 * u, x);
                     tc::tmem_wait_ld();
-                    if (grows) decayed(u, x);
+                    if (!plain) decayed(u, x);
                     const int last = u < blk ? 31 : lane;  // (behind the diagonal: keys the row does not see)
 #pragma unroll
                     for (int j = 0; j < 32; j += 2)
                         mx = fmax3(mx, j <= last ? fabsf(x[j]) : 0.f, j + 1 <= last ? fabsf(x[j + 1]) : 0.f);
                 }
-                f = to_middle(grows ? mx : mx * fast_exp2(a.log2_scale), -100, 100);
+                f = to_middle(!plain ? mx : mx * fast_exp2(a.log2_scale), -100, 100);
                 s.ps[b][i] = f;
             }
             // P over the scores: block u goes to columns 16 u .. 16 u + 15, all read by then

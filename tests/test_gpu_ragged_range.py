@@ -346,3 +346,9 @@ def _reset_and_growth(dt, dims):
 @pytest.mark.parametrize("dims", [(16, 64), (128, 64)])
 def test_linear_attention_growth_does_not_undo_a_reset(dt, dims):
     _reset_and_growth(dt, dims)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dv", [64, 128])
+def test_linear_attention_growth_does_not_undo_a_reset_key_dim_64(dt, dv):
+    _reset_and_growth(dt, (64, dv))
