@@ -52,7 +52,7 @@ attn_packed_simt_kernel(const T* __restrict__ q, long long ldq, const T* __restr
     PackedSimtSmem<DH, DV, QT>& sm = *reinterpret_cast<PackedSimtSmem<DH, DV, QT>*>(packed_simt_raw);
     constexpr int RT = QT / 16;  // rows per thread
     const int h = blockIdx.x % H, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const ragged::Item it = ragged::find_item<NT>(sm.find, cu, n_seqs, total, QT, false, blockIdx.x / H, status);
+    const ragged::Item it = ragged::find_item<NT>(sm.find, cu, n_seqs, total, QT, blockIdx.x / H, status);
     if (it.seq < 0) return;
     const int L = it.len;
     const int i0 = ((L + QT - 1) / QT - 1 - it.tile) * QT;

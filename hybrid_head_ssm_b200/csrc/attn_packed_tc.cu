@@ -55,8 +55,8 @@ struct Weights {
     static constexpr float LOW = std::is_same<T, bf16>::value ? 0.f : 11.f;
     static constexpr float TOP = std::is_same<T, bf16>::value ? 8.f : 15.f;
 };
-// TMEM columns: O_A [0,128), O_B [128,256), S_A [256,384), S_B [384,512); P_t in the first
-// 64 columns of S_t (128 16-bit keys per row, two per column)
+// TMEM columns: O_A [0,128), O_B [128,256), S_A [256,384), S_B [384,512). S_t holds two steps of
+// 64 keys, 64 columns each; a step's P lies in the first 32 of its columns (two 16-bit keys each)
 constexpr uint32_t TM_O = 0, TM_S = 256;
 
 // Ring depth: three stages of K and V where the Q/K dim leaves room for them, else two.
@@ -229,7 +229,7 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     // setup above touches no global memory; everything below may read the previous
     // kernel's output
     griddep_sync();
-    const ragged::Item it = ragged::find_item<NT>(s.find, a.cu, a.n_seqs, a.total, 2 * QT, false, blockIdx.x / a.H, status);
+    const ragged::Item it = ragged::find_item<NT>(s.find, a.cu, a.n_seqs, a.total, 2 * QT, blockIdx.x / a.H, status);
     if (it.seq < 0) return;
     const int L = it.len;
     const int i0 = ((L + 2 * QT - 1) / (2 * QT) - 1 - it.tile) * 2 * QT;  // the heaviest rows first

@@ -170,6 +170,7 @@ struct LinAttn {
     int n_seqs, total, Hk, H, dk, dv;
     float scale;
 };
+// Single tokens of any type, packed prompts of fp32 rows.
 template <typename T>
 int launch_linattn_recurrent(const Ctx& ctx, const LinAttn& a);
 // Packed prompts of 16-bit rows in chunks of 64 rows, tensor cores.

@@ -17,7 +17,7 @@ namespace {
 
 constexpr int NT = 128;  // 4 warps
 
-template <typename T, int DK, int VR>
+template <typename T, int DK, int VR, bool PACKED>
 __global__ void __launch_bounds__(NT)
 linattn_recurrent_kernel(const T* __restrict__ q, long long ldq, const T* __restrict__ k, long long ldk,
                          const T* __restrict__ v, long long ldv, const float* __restrict__ g, long long ldg,
@@ -31,11 +31,11 @@ linattn_recurrent_kernel(const T* __restrict__ q, long long ldq, const T* __rest
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane % LPR, rsub = lane / LPR;
     const int h = blockIdx.y, hk = h / (H / Hk);
-    const int s = cu ? ragged::longest_first(cu, gridDim.z, total, blockIdx.z) : blockIdx.z;
+    const int s = PACKED ? ragged::longest_first(cu, gridDim.z, total, blockIdx.z) : blockIdx.z;
     const int r0 = (blockIdx.x * (NT / 32) + warp) * VR;  // the warp's first v row
     if (r0 >= dv) return;
     int start = s, len = 1;
-    if (cu && !ragged::sequence(cu, s, total, &start, &len)) {
+    if (PACKED && !ragged::sequence(cu, s, total, &start, &len)) {
         if (threadIdx.x == 0) set_status(status, HYMBA_ERR_DEVICE_RANGE);
         return;
     }
@@ -85,23 +85,31 @@ linattn_recurrent_kernel(const T* __restrict__ q, long long ldq, const T* __rest
     }
 }
 
-template <typename T, int DK>
-int launch_dk(const Ctx& ctx, const LinAttn& a) {
+template <typename T, int DK, bool PACKED>
+int launch_form(const Ctx& ctx, const LinAttn& a) {
     constexpr int VR = 16;
-    auto kern = linattn_recurrent_kernel<T, DK, VR>;
+    auto kern = linattn_recurrent_kernel<T, DK, VR, PACKED>;
     // sequences on the grid's slowest dimension, in runs it can hold
     for (int s0 = 0; s0 < a.n_seqs; s0 += 65535) {
         const int n = a.n_seqs - s0 < 65535 ? a.n_seqs - s0 : 65535;
-        const long long row0 = a.cu ? 0 : s0;
+        const long long row0 = PACKED ? 0 : s0;
         const long long st0 = (long long)s0 * a.H * a.dv * DK;
-        HYMBA_LAUNCH(ctx, a.cu ? "linattn_recurrent" : "linattn_step", kern,
+        HYMBA_LAUNCH(ctx, PACKED ? "linattn_recurrent" : "linattn_step", kern,
                      dim3(ceil_div(a.dv, VR * (NT / 32)), a.H, n), NT, 0, static_cast<const T*>(a.q) + row0 * a.ldq,
                      a.ldq, static_cast<const T*>(a.k) + row0 * a.ldk, a.ldk, static_cast<const T*>(a.v) + row0 * a.ldv,
-                     a.ldv, a.g + row0 * a.ldg, a.ldg, a.cu ? a.cu + s0 : nullptr, a.total,
+                     a.ldv, a.g + row0 * a.ldg, a.ldg, PACKED ? a.cu + s0 : nullptr, a.total,
                      a.state_in ? a.state_in + st0 : nullptr, a.state_out ? a.state_out + st0 : nullptr,
                      static_cast<T*>(a.o) + row0 * a.ldo, a.ldo, a.Hk, a.H, a.dv, a.scale, ctx.status);
     }
     return HYMBA_OK;
+}
+
+template <typename T, int DK>
+int launch_dk(const Ctx& ctx, const LinAttn& a) {
+    if constexpr (sizeof(T) == 4) {
+        if (a.cu) return launch_form<T, DK, true>(ctx, a);
+    }
+    return launch_form<T, DK, false>(ctx, a);
 }
 
 }  // namespace

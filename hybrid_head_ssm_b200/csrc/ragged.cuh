@@ -44,8 +44,9 @@ struct FindSmem {
     Item item;
 };
 
-// find_item for up to 32 sequences: every warp for itself, one round trip, no barrier. `report`:
-// whether this warp records offsets that are out of order.
+// The t-th work item of up to 32 sequences, each cut into ceil(len / rows) runs (min_one: at least
+// one, so that empty sequences are items too): every warp for itself, one round trip, no
+// barrier. `report`: whether this warp records offsets that are out of order.
 __device__ __forceinline__ Item find_item32(const int* cu, int n_seqs, int total, int rows, bool min_one, long long t,
                                             bool report, int* status) {
     const int lane = threadIdx.x & 31;
@@ -74,15 +75,13 @@ __device__ __forceinline__ Item find_item32(const int* cu, int n_seqs, int total
     return it;
 }
 
-// The t-th work item when every sequence is cut into ceil(len / rows) runs (min_one: at
-// least one, so that empty sequences are items too). Called by all NT threads of the
+// The t-th work item when every sequence is cut into ceil(len / rows) runs. Called by all NT threads of the
 // block; each thread counts a run of consecutive sequences and one block scan finds the
 // sequence, so the cost is a few memory round trips for any number of sequences.
 template <int NT>
-__device__ Item find_item(FindSmem& sm, const int* cu, int n_seqs, int total, int rows, bool min_one, long long t,
-                          int* status) {
+__device__ Item find_item(FindSmem& sm, const int* cu, int n_seqs, int total, int rows, long long t, int* status) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (n_seqs <= 32) return find_item32(cu, n_seqs, total, rows, min_one, t, blockIdx.x == 0 && warp == 0, status);
+    if (n_seqs <= 32) return find_item32(cu, n_seqs, total, rows, false, t, blockIdx.x == 0 && warp == 0, status);
     const int per = (n_seqs + NT - 1) / NT;
     const int s0 = min(tid * per, n_seqs), s1 = min(s0 + per, n_seqs);
     if (tid == 0) sm.item.seq = -1;
@@ -90,8 +89,7 @@ __device__ Item find_item(FindSmem& sm, const int* cu, int n_seqs, int total, in
     for (int s = s0; s < s1; ++s) {
         int a, n;
         if (sequence(cu, s, total, &a, &n)) {
-            const int c = (n + rows - 1) / rows;
-            mine += min_one && c == 0 ? 1 : c;
+            mine += (n + rows - 1) / rows;
         } else if (blockIdx.x == 0) {
             set_status(status, HYMBA_ERR_DEVICE_RANGE);
         }
@@ -110,8 +108,7 @@ __device__ Item find_item(FindSmem& sm, const int* cu, int n_seqs, int total, in
         for (int s = s0; s < s1; ++s) {
             int a, n;
             if (!sequence(cu, s, total, &a, &n)) continue;
-            int c = (n + rows - 1) / rows;
-            if (min_one && c == 0) c = 1;
+            const int c = (n + rows - 1) / rows;
             if (t < before + c) {
                 sm.item.seq = s;
                 sm.item.start = a;
