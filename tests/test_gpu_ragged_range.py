@@ -352,3 +352,94 @@ def test_linear_attention_growth_does_not_undo_a_reset(dt, dims):
 @pytest.mark.parametrize("dv", [64, 128])
 def test_linear_attention_growth_does_not_undo_a_reset_key_dim_64(dt, dv):
     _reset_and_growth(dt, (64, dv))
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dims", [(16, 64), (128, 128)])
+def test_linear_attention_decays_of_other_key_dims(dt, dims):
+    """As test_linear_attention_decays, for the key dims it does not have, and rows that forget again and again."""
+    torch, hy, rt, code, tdt = _mods()
+    lens, Hk, H, (dk, dv) = [200, 70], 2, 4, dims
+    x = _linear(dt, lens, Hk, H, dk, dv, 53)
+    q, k, v, g, st, cu = x
+    n = sum(lens)
+    per_head = torch.tensor([-1e-3, -0.1, 0.0, -3.0], device="cuda")
+    reset = g.clone() * 0.01
+    for r in (0, 30, 31, 100, 200, 250):
+        reset[r] = float("-inf")
+    often = g.clone()
+    often[::3] = float("-inf")
+    often[1::7] = -90.0
+    huge = g.clone() * 0.01
+    huge[50] = -1e30
+    huge[120] = -5000.0
+    for name, gg in (("per head", per_head), ("broadcast", per_head.expand(q.shape[0], H)), ("resets", reset), ("huge", huge),
+                     ("often", often)):
+        o, end = _run_linear(dt, x, Hk, H, dk, dv, True, g=gg)
+        _status_ok(hy, torch)
+        full = _np(gg.expand(q.shape[0], H))
+        want, oa, we, ea = ro.linear_attention(_np(q), _np(k), _np(v), full, _offsets(lens), Hk, H, dk ** -0.5, _np(st))
+        ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
+        _hold(_np(o)[:n], want[:n], ob[:n], f"{dt} {name} o", 2 * U[dt] + 2.0 ** -17)
+        _hold(_np(end), we, eb, f"{dt} {name} state", 2.0 ** -16)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dims", [(16, 64), (128, 128)])
+@pytest.mark.parametrize("spread", [1e-3, 30.0])
+def test_linear_attention_small_and_large_values_of_other_key_dims(dt, dims, spread):
+    torch, hy, rt, code, tdt = _mods()
+    lens, Hk, H, (dk, dv) = [150, 70], 2, 2, dims
+    x = _linear(dt, lens, Hk, H, dk, dv, 52, decay=0.05, spread=spread)
+    scale = 1.0 if spread < 1 else 1e-4
+    q, k, v, g, st, cu = x
+    st.mul_(spread * spread)
+    o, end = _run_linear(dt, x, Hk, H, dk, dv, True, scale=scale)
+    _status_ok(hy, torch)
+    want, oa, we, ea = ro.linear_attention(_np(q), _np(k), _np(v), _np(g), _offsets(lens), Hk, H, scale, _np(st))
+    ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
+    n = sum(lens)
+    _hold(_np(o)[:n], want[:n], ob[:n], f"{dt} o")
+    _hold(_np(end), we, eb, f"{dt} state", 2.0 ** -16)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("dims", [(16, 64), (128, 64)])
+def test_linear_attention_offsets_out_of_order_of_other_key_dims(dt, dims):
+    torch, hy, rt, code, tdt = _mods()
+    Hk, H, (dk, dv) = 2, 2, dims
+    for bad in ([0, 40, 200], [0, 40, 30], [-5, 40, 60]):
+        x = list(_linear(dt, [60, 40], Hk, H, dk, dv, 55, pad=0))
+        x[5] = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        o, end = _run_linear(dt, x, Hk, H, dk, dv, True)
+        torch.cuda.synchronize()
+        assert hy.hymba_get_device_status(None) == hy.HYMBA_ERR_DEVICE_RANGE
+        assert end[0 if bad[0] < 0 else 1].isnan().all(), bad  # not written
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("dims", [(16, 64), (128, 64)])
+def test_linear_attention_many_short_prompts_captured_of_other_key_dims(dt, dims):
+    """More sequences than a warp has lanes, captured into a graph and replayed on another stream."""
+    torch, hy, rt, code, tdt = _mods()
+    Hk, H, (dk, dv) = 1, 3, dims
+    lens = [(7 * i) % 40 for i in range(70)]
+    x = _linear(dt, lens, Hk, H, dk, dv, 59)
+    q, k, v, g, st, cu = x
+    o, end = _run_linear(dt, x, Hk, H, dk, dv, True)
+    want, oa, we, ea = ro.linear_attention(_np(q), _np(k), _np(v), _np(g), _offsets(lens), Hk, H, dk ** -0.5, _np(st))
+    ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
+    n = sum(lens)
+    _hold(_np(o)[:n], want[:n], ob[:n], f"{dt} o", 2 * U[dt] + 2.0 ** -17)
+    _hold(_np(end), we, eb, f"{dt} state", 2.0 ** -16)
+    s = hy.linattn_shape(Hk, H, dk, dv, code[dt])
+    ws = rt.linattn_workspace(s, len(lens), q.shape[0])
+    o2, end2 = torch.full_like(o, 7.0), torch.zeros_like(end)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rt.linattn_prefill(s, q, k, v, g, cu, o2, ws, state_in=st, state_out=end2)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        graph.replay()
+    _status_ok(hy, torch)
+    assert torch.equal(o, o2) and torch.equal(end, end2)
