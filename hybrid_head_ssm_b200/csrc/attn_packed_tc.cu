@@ -121,32 +121,6 @@ __device__ __forceinline__ void fail(volatile int* abort, int* status, int role,
     tc::record_timeout(status, role, step, bar);
 }
 
-// Whether the lane's share of PIECES 16-byte pieces holds a value that is infinite or NaN: 0 x it
-// is NaN, and a sum of such products stays NaN. Eight loads in flight: one at a time, a block
-// of V took longer to look through than its softmax.
-template <bool BF16, int PIECES>
-__device__ __forceinline__ bool any_odd(const uint4* v, int lane) {
-    typedef typename std::conditional<BF16, __nv_bfloat162, __half2>::type P2;
-    const uint32_t nul = 0u;
-    uint32_t acc[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 1
-    for (int x = lane; x < PIECES; x += 32 * 8) {
-        uint4 w[8];
-#pragma unroll
-        for (int y = 0; y < 8; ++y) w[y] = v[x + 32 * y];
-#pragma unroll
-        for (int y = 0; y < 8; ++y) {
-            const uint32_t ww[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const P2 r = __hfma2(*reinterpret_cast<const P2*>(&ww[i]), *reinterpret_cast<const P2*>(&nul),
-                                     *reinterpret_cast<const P2*>(&acc[i]));
-                acc[i] = *reinterpret_cast<const uint32_t*>(&r);
-            }
-        }
-    }
-    return ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0;
-}
 template <bool BF16>
 __device__ __forceinline__ uint32_t drop_odd(uint32_t w) {
     constexpr uint32_t E = BF16 ? 0x7f807f80u : 0x7c007c00u;
@@ -398,7 +372,7 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                     if (k0 + KB > L)
                         for (int x = lane; x < PIECES; x += 32)
                             if (k0 + ((x >> 3) & (KB - 1)) >= L) vb[x] = make_uint4(0, 0, 0, 0);
-                    if (__any_sync(0xffffffffu, any_odd<BF16, PIECES>(vb, lane))) {
+                    if (__any_sync(0xffffffffu, ragged::any_odd<BF16, PIECES>(vb, lane))) {
                         for (int x = lane; x < PIECES; x += 32) {
                             uint4 w = vb[x];
                             w.x = drop_odd<BF16>(w.x);

@@ -40,6 +40,10 @@ namespace hymba {
 
 namespace {
 
+using ragged::fade;
+using ragged::inverse;
+using ragged::to_middle;
+
 constexpr int CQ = 64;   // rows per chunk
 constexpr int CV = 64;   // value columns per CTA
 constexpr int NT = 128;  // 4 warps
@@ -111,17 +115,6 @@ struct Stager {
     }
 };
 
-// a power of two that brings x (> 0) near 2^12, within 2^low and 2^high; 1 for 0 and what is
-// not finite
-__device__ __forceinline__ float to_middle(float x, int low, int high) {
-    const int e = (__float_as_int(x) >> 23) & 255;
-    if (e == 0 || e == 255) return 1.f;
-    return __int_as_float((127 + min(max(127 - e + 12, low), high)) << 23);
-}
-
-// a decay of 0 drops what it multiplies, also what is not finite
-__device__ __forceinline__ float fade(float d, float x) { return d == 0.f ? 0.f : d * x; }
-
 template <typename T> struct Pair;
 template <> struct Pair<f16> { typedef __half2 type; };
 template <> struct Pair<bf16> { typedef __nv_bfloat162 type; };
@@ -131,9 +124,6 @@ __device__ __forceinline__ typename Pair<T>::type pair(uint32_t x) {
 }
 template <typename P2>
 __device__ __forceinline__ uint32_t bits(P2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
-
-// the inverse of a power of two: its exponent mirrored
-__device__ __forceinline__ float inverse(float p) { return __int_as_float(0x7f000000 - __float_as_int(p)); }
 
 __device__ __forceinline__ void scale_rows(float (&x)[2][4], float a, float b) {
 #pragma unroll
@@ -173,7 +163,8 @@ __device__ __noinline__ float row_product(const Tables& tab, const uint8_t* p, c
 // The state after a chunk, row by row in fp32 over the rows it still sees: S is the warp's share, val its
 // first value column of the tile.
 template <typename T, int DK>
-__device__ __forceinline__ void row_states(const Tables& tab, const uint8_t* k, const uint8_t* v, int val, float (&S)[DK / 8][4]) {
+__device__ __forceinline__ void row_states(const Tables& tab, const uint8_t* k, const uint8_t* v, int val,
+                                           float (&S)[DK / 8][4]) {
     const int lq = threadIdx.x & 3;
 #pragma unroll
     for (int n = 0; n < DK / 8; ++n)

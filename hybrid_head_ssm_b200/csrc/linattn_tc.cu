@@ -51,6 +51,10 @@ namespace hymba {
 
 namespace {
 
+using ragged::fade;
+using ragged::inverse;
+using ragged::to_middle;
+
 constexpr int CQ = 128;  // rows per chunk
 constexpr int DK = 64;
 constexpr int NT = 512;
@@ -117,17 +121,6 @@ __device__ __forceinline__ void fail(volatile int* abort, int* status, int role,
     tc::record_timeout(status, role, step, bar);
 }
 
-// a power of two that brings x (> 0) near 2^12, within 2^low and 2^high; 1 for 0 and what is
-// not finite
-__device__ __forceinline__ float to_middle(float x, int low, int high) {
-    const int e = (__float_as_int(x) >> 23) & 255;
-    if (e == 0 || e == 255) return 1.f;
-    return __int_as_float((127 + min(max(127 - e + 12, low), high)) << 23);
-}
-// the inverse of a power of two: its exponent mirrored
-__device__ __forceinline__ float inverse(float p) { return __int_as_float(0x7f000000 - __float_as_int(p)); }
-// a decay of 0 drops what it multiplies, also what is not finite
-__device__ __forceinline__ float fade(float d, float x) { return d == 0.f ? 0.f : d * x; }
 
 template <typename T>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -525,33 +518,14 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 break;
             }
             const int n = len - c * CQ;
-            // 0 x (not finite) is NaN; 16-byte piece x of panel p: row x / 8
-            typedef typename std::conditional<F16, __half2, __nv_bfloat162>::type P2;
+            // 16-byte piece x of panel p: row x / 8
             uint4* vb = reinterpret_cast<uint4*>(s.v[b][0]);
             constexpr int PIECES = CQ * 8 * (DV / 64);
             if (n < CQ)
                 for (int x = lane; x < PIECES; x += 32)
                     if (((x >> 3) & (CQ - 1)) >= n) vb[x] = make_uint4(0, 0, 0, 0);
-            uint32_t acc[4] = {0u, 0u, 0u, 0u};
-            const uint32_t nul = 0u;
-#pragma unroll 1
-            for (int x = lane; x < PIECES; x += 32 * 8) {
-                uint4 w[8];
-#pragma unroll
-                for (int y = 0; y < 8; ++y) w[y] = vb[x + 32 * y];
-#pragma unroll
-                for (int y = 0; y < 8; ++y) {
-                    const uint32_t ww[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const P2 r = __hfma2(*reinterpret_cast<const P2*>(&ww[i]), *reinterpret_cast<const P2*>(&nul),
-                                             *reinterpret_cast<const P2*>(&acc[i]));
-                        acc[i] = *reinterpret_cast<const uint32_t*>(&r);
-                    }
-                }
-            }
-            const bool odd = ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0;
-            if (__any_sync(0xffffffffu, odd) && lane == 0) *reinterpret_cast<volatile int*>(&s.dirty) = 1;
+            if (__any_sync(0xffffffffu, ragged::any_odd<!F16, PIECES>(vb, lane)) && lane == 0)
+                *reinterpret_cast<volatile int*>(&s.dirty) = 1;
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(&s.v_ok[b]);
         }

@@ -1,6 +1,6 @@
 // Pieces shared by the kernels of ragged batches (packed prompts, paged K/V, linear
-// attention): work items of packed sequences, 16-byte row loads, fragments of either
-// 16-bit type.
+// attention): work items of packed sequences, powers of two for fp16's range, a look for values
+// that are not finite, 16-byte row loads of any type.
 #pragma once
 #include "common.cuh"
 #include "warp_mma.cuh"
@@ -123,6 +123,44 @@ __device__ Item find_item(FindSmem& sm, const int* cu, int n_seqs, int total, in
     return sm.item;
 }
 
+// a power of two that brings x (> 0) near 2^12, within 2^low and 2^high; 1 for 0 and what is
+// not finite
+__device__ __forceinline__ float to_middle(float x, int low, int high) {
+    const int e = (__float_as_int(x) >> 23) & 255;
+    if (e == 0 || e == 255) return 1.f;
+    return __int_as_float((127 + min(max(127 - e + 12, low), high)) << 23);
+}
+// the inverse of a power of two: its exponent mirrored
+__device__ __forceinline__ float inverse(float p) { return __int_as_float(0x7f000000 - __float_as_int(p)); }
+// a decay of 0 drops what it multiplies, also what is not finite
+__device__ __forceinline__ float fade(float d, float x) { return d == 0.f ? 0.f : d * x; }
+
+// Whether the lane's share of PIECES 16-byte pieces holds a value that is infinite or NaN: 0 x it
+// is NaN, and a sum of such products stays NaN. Eight loads in flight: one at a time, a block
+// of V took longer to look through than its softmax.
+template <bool BF16, int PIECES>
+__device__ __forceinline__ bool any_odd(const uint4* v, int lane) {
+    typedef typename std::conditional<BF16, __nv_bfloat162, __half2>::type P2;
+    const uint32_t nul = 0u;
+    uint32_t acc[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+    for (int x = lane; x < PIECES; x += 32 * 8) {
+        uint4 w[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) w[y] = v[x + 32 * y];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+            const uint32_t ww[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const P2 r = __hfma2(*reinterpret_cast<const P2*>(&ww[i]), *reinterpret_cast<const P2*>(&nul),
+                                     *reinterpret_cast<const P2*>(&acc[i]));
+                acc[i] = *reinterpret_cast<const uint32_t*>(&r);
+            }
+        }
+    }
+    return ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0;
+}
 // 8 consecutive elements as fp32 (one or two 16-byte loads)
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
