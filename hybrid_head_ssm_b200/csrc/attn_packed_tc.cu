@@ -21,8 +21,8 @@
 //               2^(s - m) as 16-bit pairs, the row sum of the fp32 values; O is rescaled in
 //               TMEM only when the running max grows by more than 2^4 (fp16) or 2^8 (bf16).
 // A CTA that noted a value that is not finite computes its rows once more from global
-// memory, key by key over what each row sees; so does a row whose sums are not finite (a visible
-// infinity times a weight that rounds to 0 in 16 bits).
+// memory, key by key over what each row sees. A row whose sums are not finite though its weights are
+// looks through the V that it sees: an infinity times a weight that rounds to 0 in 16 bits was NaN.
 // P is rounded to the rows' type, as an MMA operand has to be: half a step relative to each
 // weight, the size of the output's own rounding. fp16 has little range: m is the running max less
 // 11, so that P lies between 2^11 and 2^15 at the largest weight and keeps all its bits down to
@@ -160,6 +160,34 @@ __device__ __noinline__ void recompute_row(const T* q, const T* k, long long ldk
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[c0 + e] = from_f<T>(inv == 0.f ? 0.f : acc[e] * inv);
+    }
+}
+
+// The columns of one row where V holds infinities that it sees: weights of finite scores are above 0, so
+// their sum is what the infinities add up to. `none`: no score above -infinity, the row is zero.
+template <typename T, int DV>
+__device__ __noinline__ void infinite_columns(const T* v, long long ldv, T* o, int i, int n_meta, int window, bool none) {
+    const int meta_e = min(n_meta, i + 1), wa = window > 0 ? max(n_meta, i - window + 1) : n_meta;
+#pragma unroll 1
+    for (int c0 = 0; c0 < DV; c0 += 8) {
+        float acc[8] = {};
+        bool numbers = !none;  // a column is not NaN yet
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part)
+#pragma unroll 1
+            for (int j = part ? wa : 0; numbers && j < (part ? i + 1 : meta_e); ++j) {
+                float y[8];
+                ragged::load8(v + j * ldv + c0, y);
+                numbers = false;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    acc[e] += isfinite(y[e]) ? 0.f : y[e];
+                    numbers |= acc[e] == acc[e];
+                }
+            }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (none || acc[e] != 0.f) o[c0 + e] = from_f<T>(acc[e]);
     }
 }
 
@@ -532,11 +560,14 @@ attn_packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 }
                 __syncwarp();
             }
-            if (i < L && (!(odd == 0.f) || *reinterpret_cast<volatile int*>(&s.dirty)))
+            if (i < L && *reinterpret_cast<volatile int*>(&s.dirty))
                 recompute_row<T, DH, DV>(static_cast<const T*>(a.q) + (it.start + (long long)i) * a.ldq + (long long)h * DH,
                                          static_cast<const T*>(a.k) + it.start * a.ldk + (long long)g * DH, a.ldk,
                                          static_cast<const T*>(a.v) + it.start * a.ldv + (long long)g * DV, a.ldv, orow, i,
                                          n_meta, window, scale, m_used == -INFINITY ? 0.f : m_used, inv);
+            else if (i < L && !(odd == 0.f) && l - l == 0.f)
+                infinite_columns<T, DV>(static_cast<const T*>(a.v) + it.start * a.ldv + (long long)g * DV, a.ldv, orow, i,
+                                        n_meta, window, l == 0.f);
         } else if (ok && nt > 0) {
             if (lane == 0) fail(abort, status, 2, nt, 8);
         }

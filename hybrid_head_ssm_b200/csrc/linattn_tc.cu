@@ -35,9 +35,9 @@
 // Few long sequences are cut into segments of whole chunks (`segment_rows`): the same kernel first
 // forms what each segment adds to a state of zero, a small one turns these into the state before
 // each segment, and the segments then run side by side.
-// A CTA that noted a value of V, or of a row of K that the state takes up, that is not finite computes
-// its rows once more by the recurrence, in which nothing reaches a row that does not see it and an
-// infinity stays one (its parts would be infinity minus infinity).
+// A CTA that noted a value of V that is not finite, or an infinity in a row of K that the state takes
+// up, computes its rows once more by the recurrence, in which nothing reaches a row that does not see it
+// and an infinity stays one (its parts would be infinity minus infinity).
 // Bound: HBM (q, k, v read and o written once per 128 value columns); what is left is the chain of a
 // chunk, about 6900 clocks, and the last sequences' chunks alone. Eight prompts of up to 4224 rows
 // (19800 in all), 25 heads of 64 x 128, bf16: 124 us, 49% of the copy rate.
@@ -261,7 +261,7 @@ __device__ __noinline__ void recurrence(const Args& a, const float* from, float*
 }
 
 // Row r of K' = w k as parts of T; w = 0 drops the row. The 16-byte pieces are swizzled by the row.
-// Returns whether the row holds a value that is not finite (bf16; of fp16's the largest is looked at).
+// Returns whether the row holds an infinity (bf16; of fp16's the largest is looked at).
 template <typename T, int PARTS>
 __device__ __forceinline__ bool scaled_keys(uint8_t (*ks)[TILE], const uint8_t* krow, int r, float w) {
     const float2 w2 = make_float2(w, w);
@@ -292,7 +292,12 @@ __device__ __forceinline__ bool scaled_keys(uint8_t (*ks)[TILE], const uint8_t* 
         for (int p = 0; p < PARTS; ++p)
             *reinterpret_cast<uint4*>(ks[p] + r * 128 + at) = make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
     }
-    return !drop && (*reinterpret_cast<const uint32_t*>(&odd) & 0x7fff7fffu) != 0;
+    if (drop || (*reinterpret_cast<const uint32_t*>(&odd) & 0x7fff7fffu) == 0) return false;
+    const uint32_t* kw = reinterpret_cast<const uint32_t*>(krow);
+    bool inf = false;
+#pragma unroll 1
+    for (int x = 0; x < 32; ++x) inf |= __vcmpeq2(kw[x] & 0x7fff7fffu, 0x7f807f80u) != 0;
+    return inf;
 }
 
 // the power of two of a chunk's K' from its four warps' largest values. Down as far as weights above 1

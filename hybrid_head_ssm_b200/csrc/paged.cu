@@ -503,13 +503,16 @@ __global__ void __launch_bounds__(128, blocks_per_sm(DH + DV, NG)) decode_paged_
     constexpr int LD = DV + 4;
     float* acc = reinterpret_cast<float*>(decode_raw);  // [4][8 NG][LD]
     static_assert(4 * 8 * NG * LD * 4 <= 4 * R_::SIZE, "the joined sums reuse the rings");
-    float odd = 0.f;  // NaN once a sum is not finite
+    float odd = 0.f;  // NaN once a sum of a head whose weights are finite is not
 #pragma unroll
     for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int t = 0; t < DV / 16; ++t)
+        for (int e = 0; e < 4; ++e) {
+            float z = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) odd = fmaf(ot[n][t][e], 0.f, odd);
+            for (int t = 0; t < DV / 16; ++t) z = fmaf(ot[n][t][e], 0.f, z);
+            if (l[n][e & 1] - l[n][e & 1] == 0.f) odd += z;
+        }
     const bool again = __any_sync(0xffffffffu, !(odd == 0.f));
     if (again)
         sums_again<T, DH, DV, 8 * NG, LD>(a, w, b, g, h0, nh, k0, k1, ms, ls, acc + warp * 8 * NG * LD);
