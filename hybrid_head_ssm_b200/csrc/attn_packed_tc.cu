@@ -28,8 +28,9 @@
 // 11, so that P lies between 2^11 and 2^15 at the largest weight and keeps all its bits down to
 // 2^-25 of it (below, half of fp16's smallest step: 2^-36 of it); the factor leaves with the row sum.
 // Bound by the tensor cores (2 (dh + dv) flops per visible pair); what is left is the softmax's
-// instruction issue, about 1500 clocks per 64 keys and tile with two tiles on the SM's four
-// schedulers, and in windows a block's start and end, about 10,000 clocks. 25 heads of 64 x 128:
+// latency, about 1500 clocks per 64 keys and tile: two warps per scheduler do not cover their own
+// waits (XU pipe 61 %, issue slots 43 %, tensor pipe 46 % busy), and in windows a block's start and
+// end, about 10,000 clocks. 25 heads of 64 x 128:
 // three prompts of up to 8320 rows, whole history (bf16), 840 us, 53% of the bf16 rate; eight of up
 // to 4224, window 1024 and 128 meta tokens (f16), 282 us, 39%. Part of the exponentials as
 // polynomials on the FMA pipe: 869 us for a quarter of them, 910 for half, 829 then for none.

@@ -31,8 +31,8 @@
 // Bound: HBM (q, k, v once per 64 value columns, o) and the warp MMAs (1024 multiply-adds per
 // clock and SM measured) are close; what is left is instruction issue, hence the tables that
 // one warp (the one with the fewest tiles of P) forms a chunk ahead for all. Eight prompts of 2000
-// rows, bf16: 50 heads of 16 x 64 with shared keys 107 us (their 212 MB take 32), 25 of 128 x 128
-// with 5 key heads 339 us.
+// rows, bf16: 50 heads of 16 x 64 with shared keys 112 us (their 212 MB take 32), 25 of 128 x 128
+// with 5 key heads 310 to 350 us from one process to the next (fp16 121 and 313 to 319).
 #include "kernels.h"
 #include "ragged.cuh"
 

@@ -322,13 +322,15 @@ int hymba_attn_decode_static(const hymba_layer_cfg* cfg, const void* q, int64_t 
  * descending, within 0 .. total_rows; empty sequences are allowed). Rows that belong to
  * no sequence are neither used nor written. A sequence whose offsets break that rule is
  * left out (its rows are not written, its state neither) and HYMBA_ERR_DEVICE_RANGE is
- * recorded in the status word.
+ * recorded in the status word. Where offsets that descend make other sequences overlap, which of
+ * them writes a shared row is not defined, and a call may leave some of their rows out.
  *
  * Element types: HYMBA_F16 (the type of K and V inside a bf16 layer), HYMBA_BF16 and
  * HYMBA_F32. Products of 16-bit operands run on the tensor cores with fp32
  * accumulation, fp32 ones on the CUDA cores; softmax statistics and states are fp32.
  * Values at places that a row does not see, non-finite ones among them, do not reach
- * the row's output. All calls only queue work on `stream`: they can be captured into a
+ * the row's output. An infinite value that it sees gives an infinity (or NaN, with others), which
+ * takes a slower path than finite ones. All calls only queue work on `stream`: they can be captured into a
  * graph, and calls on different streams may overlap as long as they share no output and
  * no workspace.
  * --------------------------------------------------------------------------- */
@@ -386,8 +388,8 @@ typedef struct hymba_paged_kv {
  * k [total_rows, n_kv_heads * head_dim] and v [total_rows, n_kv_heads * v_head_dim] become
  * its newest positions len[b] - n_b .. len[b] - 1: len already counts them (the caller
  * advances it, on the same stream, before the call). cu_seqlens NULL: one row per
- * sequence, total_rows = batch. A row whose position or page is out of range is not
- * written and HYMBA_ERR_DEVICE_RANGE is recorded. Rows of two sequences that meet in one
+ * sequence, total_rows = batch. A row whose position is negative, whose page is out of range or
+ * whose sequence's len is past the table is not written and HYMBA_ERR_DEVICE_RANGE is recorded. Rows of two sequences that meet in one
  * slot race: one of them stays. */
 int hymba_kv_append_paged(const hymba_paged_kv* kv, const void* k, int64_t ldk, const void* v, int64_t ldv,
                           const int32_t* cu_seqlens, int total_rows, void* stream);
@@ -412,7 +414,9 @@ size_t hymba_attn_decode_paged_workspace(const hymba_attn_shape* shape, int batc
 /* Linear attention with a decay for each head, the recurrence of the SSD form ("Lecture
  * 04 - Beyond the Dense Transformer", section 3) with keys and queries in the place of B
  * and C: S_t = exp(g_t) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t per head, g_t the head's
- * log decay at row t (normally <= 0; -infinity forgets everything before the row).
+ * log decay at row t (normally <= 0; -infinity, like any below -104 (where exp is 0 in fp32),
+ * forgets everything before the row). A product of decays below 2^-126 may count as 0. fp16 rows
+ * enter the state scaled, which leaves its values the range up to 2^80.
  * n_qk_heads divides n_heads (at most 1024): head h reads q and k of head h / (n_heads /
  * n_qk_heads); the SSD form's shared B and C are n_qk_heads = 1. key_dim 16, 64 or 128;
  * v_head_dim a multiple of 64, at most 512 (HYMBA_ERR_UNSUPPORTED otherwise). States are
