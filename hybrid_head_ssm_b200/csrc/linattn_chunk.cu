@@ -18,7 +18,7 @@
 // Numbers: cs is summed in 64 bits. A decay between rows j <= i is 2^(a_i + b_j) with a_i and b_j
 // the fp32 distances of cs_i and cs_j from the cs at the start of i's 16 rows, and never formed from two
 // factors. A row that forgets everything (a decay that is 0 in fp32) is no term of cs but a border that
-// nothing before it passes, so the distances stay small after any number of them (only decays of 2^-100
+// nothing before it passes and at which cs starts again, so the distances stay small after any number of them (only decays of 2^-100
 // and less that are not 0, row after row, leave the others of their 16 rows right to 2^-12, half a step of
 // P). P and the copy of S that meets q are rounded to the rows' type, like any MMA operand;
 // the scaled v of the state update enters as three parts (bf16: 24 bits) or two (fp16: 22 bits, or
@@ -31,8 +31,8 @@
 // Bound: HBM (q, k, v once per 64 value columns, o) and the warp MMAs (1024 multiply-adds per
 // clock and SM measured) are close; what is left is instruction issue, hence the tables that
 // one warp (the one with the fewest tiles of P) forms a chunk ahead for all. Eight prompts of 2000
-// rows, bf16: 50 heads of 16 x 64 with shared keys 112 us (their 212 MB take 32), 25 of 128 x 128
-// with 5 key heads 310 to 350 us from one process to the next (fp16 121 and 313 to 319).
+// rows, bf16: 50 heads of 16 x 64 with shared keys 110 us (their 212 MB take 32), 25 of 128 x 128
+// with 5 key heads 302 us (fp16 119 and 345).
 #include "kernels.h"
 #include "ragged.cuh"
 
@@ -56,8 +56,13 @@ struct Tables {
     alignas(16) float w[CQ];      // 2^(cs_63 - cs_j)
     alignas(8) int border[CQ];    // the last row at or before each that forgets everything (below 0: none)
     float dec;                    // 2^cs_63
-    int resets;                   // a decay within the chunk may be 0
+    int resets;                   // a decay within the chunk may be 0; 2: some rows forget everything (border holds)
+    // the row that row i may see first
+    __device__ __forceinline__ int first(int i) const { return resets == 2 ? max(border[i], 0) : 0; }
 };
+
+// a decay below 2^-150 is 0 in fp32
+__device__ __forceinline__ bool forgets(float g) { return g < -104.f; }
 
 template <int DK>
 struct ChunkSmem {
@@ -151,7 +156,7 @@ __device__ __forceinline__ void scale_state(float (&st)[N][4], float a, float b)
 template <typename T>
 __device__ __noinline__ float row_product(const Tables& tab, const uint8_t* p, const uint8_t* v, int i, int col) {
     float sum = 0.f;
-    for (int j = max(tab.border[i], 0); j <= i; ++j) {
+    for (int j = tab.first(i); j <= i; ++j) {
         if (fast_exp2(tab.a[i] + tab.b[i >> 4][j]) == 0.f) continue;
         const T pj = *reinterpret_cast<const T*>(p + at<CQ>(i, j >> 3) + 2 * (j & 7));
         const T vj = *reinterpret_cast<const T*>(v + at<CV>(j, col >> 3) + 2 * (col & 7));
@@ -188,55 +193,65 @@ __device__ __forceinline__ void row_states(const Tables& tab, const uint8_t* k, 
     }
 }
 
-// the tables of one chunk from the two log decays each lane holds (rows 2 lane, 2 lane + 1)
-__device__ __forceinline__ void make_tables(Tables& t, float g0, float g1, float log2_scale) {
+// the tables of one chunk from the two log decays each lane holds (rows 2 lane, 2 lane + 1). BORDERS: some
+// of them forget everything; the sums start again there, so that what lies before, a NaN among it, enters
+// nothing behind
+template <bool BORDERS>
+__device__ __forceinline__ void fill_tables(Tables& t, float g0, float g1, float log2_scale) {
     constexpr double LOG2E = 1.4426950408889634;
     const int lane = threadIdx.x & 31;
-    // below 2^-150 a decay is 0 in fp32
-    const bool r0 = g0 < -104.f, r1 = g1 < -104.f;
-    const unsigned m0 = __ballot_sync(0xffffffffu, r0), m1 = __ballot_sync(0xffffffffu, r1);
+    const bool r0 = BORDERS && forgets(g0), r1 = BORDERS && forgets(g1);
     const double d0 = (double)(r0 ? 0.f : g0) * LOG2E, d1 = (double)(r1 ? 0.f : g1) * LOG2E;
-    double sum = d0 + d1;
-#pragma unroll
-    for (int w = 1; w < 32; w <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, sum, w);
-        if (lane >= w) sum += y;
-    }
-    // forward from the rows before, so that a NaN or an infinity reaches no earlier row
-    const double last = __shfl_sync(0xffffffffu, sum, 31), before = __shfl_up_sync(0xffffffffu, sum, 1);
-    const double x0 = lane ? before + d0 : d0, x1 = x0 + d1;
-    // the last row that forgets everything at or before rows 2 lane and 2 lane + 1, and in the chunk
-    int f0 = -1, f1 = -1, border = -1;
-    if (m0 | m1) {
-        const unsigned below = (1u << lane) - 1;
+    double sum = r1 ? 0.0 : d0 + d1;
+    // the last border at or before the lane's two rows and in the chunk; the first lane of its run of rows
+    int f0 = -1, f1 = -1, border = -1, head = 0;
+    if (BORDERS) {
+        const unsigned m0 = __ballot_sync(0xffffffffu, r0), m1 = __ballot_sync(0xffffffffu, r1), below = (1u << lane) - 1;
         auto row = [](unsigned even, unsigned odd) { return max(62 - 2 * __clz(even), 63 - 2 * __clz(odd)); };
         f0 = row(m0 & (below | 1u << lane), m1 & below);
         f1 = r1 ? 2 * lane + 1 : f0;
         border = row(m0, m1);
+        head = max(31 - __clz((m0 | m1) & (below | 1u << lane)), 0);
+        *reinterpret_cast<int2*>(&t.border[2 * lane]) = make_int2(f0, f1);
     }
-    float down = fminf((float)d0, 0.f) + fminf((float)d1, 0.f);
 #pragma unroll
-    for (int w = 16; w; w >>= 1) down += __shfl_xor_sync(0xffffffffu, down, w);
-    const bool resets = border >= 0 || !(down + fminf(log2_scale, 0.f) > -120.f);
+    for (int w = 1; w < 32; w <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, sum, w);
+        if (lane - w >= head) sum += y;
+    }
+    // forward from the rows before, so that a NaN or an infinity reaches no earlier row
+    const double last = __shfl_sync(0xffffffffu, sum, 31), before = __shfl_up_sync(0xffffffffu, sum, 1);
+    const double x0 = r0 ? 0.0 : lane ? before + d0 : d0, x1 = r1 ? 0.0 : x0 + d1;
     double from = 0.0;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-        const double c = b == 0 ? 0.0 : __shfl_sync(0xffffffffu, sum, b == 0 ? 0 : 8 * b - 1);
+        double c = b == 0 ? 0.0 : __shfl_sync(0xffffffffu, sum, b == 0 ? 0 : 8 * b - 1);
+        if (BORDERS && !(c - c == 0.0)) c = 0.0;  // (only a reference point: it cancels)
         if ((lane >> 3) == b) from = c;
         if ((lane >> 3) <= b)
             *reinterpret_cast<float2*>(&t.b[b][2 * lane]) = make_float2((float)(c - x0), (float)(c - x1));
     }
     *reinterpret_cast<float2*>(&t.a[2 * lane]) =
         make_float2((float)(x0 - from) + log2_scale, (float)(x1 - from) + log2_scale);
-    *reinterpret_cast<int2*>(&t.border[2 * lane]) = make_int2(f0, f1);
     *reinterpret_cast<float2*>(&t.e[2 * lane]) = make_float2(f0 >= 0 ? 0.f : fast_exp2((float)x0 + log2_scale),
                                                              f1 >= 0 ? 0.f : fast_exp2((float)x1 + log2_scale));
     *reinterpret_cast<float2*>(&t.w[2 * lane]) = make_float2(2 * lane < border ? 0.f : fast_exp2((float)(last - x0)),
                                                              2 * lane + 1 < border ? 0.f : fast_exp2((float)(last - x1)));
+    float down = fminf((float)d0, 0.f) + fminf((float)d1, 0.f);
+#pragma unroll
+    for (int w = 16; w; w >>= 1) down += __shfl_xor_sync(0xffffffffu, down, w);
     if (lane == 0) {
-        t.dec = border >= 0 ? 0.f : fast_exp2((float)last);
-        t.resets = resets;
+        t.dec = BORDERS ? 0.f : fast_exp2((float)last);
+        t.resets = BORDERS ? 2 : !(down + fminf(log2_scale, 0.f) > -120.f);
     }
+}
+// (its own function, so that the ordinary tables, on which every chunk waits, stay short)
+__device__ __noinline__ void border_tables(Tables* t, float g0, float g1, float log2_scale) {
+    fill_tables<true>(*t, g0, g1, log2_scale);
+}
+__device__ __forceinline__ void make_tables(Tables& t, float g0, float g1, float log2_scale) {
+    if (__any_sync(0xffffffffu, forgets(g0) || forgets(g1))) border_tables(&t, g0, g1, log2_scale);
+    else fill_tables<false>(t, g0, g1, log2_scale);
 }
 
 template <typename T, int DK>
@@ -363,7 +378,7 @@ linattn_chunk_kernel(const T* __restrict__ q, long long ldq, const T* __restrict
                             p[3] *= w3;
                         } else {
                             const int j = 16 * jt + 8 * n + 2 * lq;
-                            const int from0 = tab.border[16 * warp + lg], from1 = tab.border[16 * warp + lg + 8];
+                            const int from0 = tab.first(16 * warp + lg), from1 = tab.first(16 * warp + lg + 8);
                             p[0] = j < from0 ? 0.f : fade(w0, p[0]);
                             p[1] = j + 1 < from0 ? 0.f : fade(w1, p[1]);
                             p[2] = j < from1 ? 0.f : fade(w2, p[2]);

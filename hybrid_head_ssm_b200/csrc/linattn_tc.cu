@@ -25,8 +25,8 @@
 // Numbers: a decay between rows of different 32-row blocks is A_i B_j, both distances from
 // the start of i's block and so at most 1 each (a chunk with a positive log decay forms
 // 2^(a_i + b_j) instead), within a block 2^(a_i + b_j). A row that forgets everything (a decay that is 0
-// in fp32) is no term of cs but a border that nothing before it passes, so the distances stay small after
-// any number of them (only decays of 2^-100 and less that are not 0, row after row, leave the others of
+// in fp32) is no term of cs but a border that nothing before it passes and at which cs starts again, so
+// the distances stay small after any number of them (only decays of 2^-100 and less that are not 0, row after row, leave the others of
 // their block right to 2^-11, a step of P). K' enters as three parts (bf16: 24 bits) or two
 // (fp16: 22 bits, or 2^-37 of the chunk's largest weighted key where that is more); P and the state's
 // copy are rounded to the rows' type, like any MMA operand. fp16 has little range: P's rows, the copy's rows and
@@ -150,16 +150,29 @@ struct LaneTables {
             down += fminf(x, 0.f);
             up |= !(x <= 0.f);
         }
-        const double own = (d[0] + d[1]) + (d[2] + d[3]);
-        double sum = own;
+        // the sums start again at a border: what lies before it, a NaN among it, enters nothing behind it
+        const unsigned any = m[0] | m[1] | m[2] | m[3], below = (1u << lane) - 1;
+        double sum = (d[0] + d[1]) + (d[2] + d[3]);
+        int head = 0;  // the first lane of the lane's run of rows without a border
+        if (any) {
+            if ((m[1] | m[2]) >> lane & 1) sum = d[2] + d[3];
+            if (m[3] >> lane & 1) sum = 0.0;
+            head = max(31 - __clz(any & (below | 1u << lane)), 0);
+        }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const double y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
+            if (lane - o >= head) sum += y;
         }
         const double last = __shfl_sync(0xffffffffu, sum, 31);
-        const double c1 = __shfl_sync(0xffffffffu, sum, 7), c2 = __shfl_sync(0xffffffffu, sum, 15),
-                     c3 = __shfl_sync(0xffffffffu, sum, 23);
+        double c1 = __shfl_sync(0xffffffffu, sum, 7), c2 = __shfl_sync(0xffffffffu, sum, 15),
+               c3 = __shfl_sync(0xffffffffu, sum, 23);
+        if (any) {
+            // (only reference points: they cancel)
+            if (!(c1 - c1 == 0.0)) c1 = 0.0;
+            if (!(c2 - c2 == 0.0)) c2 = 0.0;
+            if (!(c3 - c3 == 0.0)) c3 = 0.0;
+        }
         const double from = blk == 0 ? 0.0 : blk == 1 ? c1 : blk == 2 ? c2 : c3;
         double before = __shfl_up_sync(0xffffffffu, sum, 1);
         if (lane == 0) before = 0.0;
@@ -170,7 +183,7 @@ struct LaneTables {
         double x = before;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            x += d[i];
+            x = m[i] >> lane & 1 ? 0.0 : x + d[i];
             a[i] = (float)(x - from) + lsc;
             b[i] = (float)(from - x);
             e[i] = fast_exp2((float)x + lsc);
@@ -186,8 +199,7 @@ struct LaneTables {
         total = last;
         dec = fast_exp2((float)last);
         border[0] = border[1] = border[2] = border[3] = -1.f;
-        if (m[0] | m[1] | m[2] | m[3]) {
-            const unsigned below = (1u << lane) - 1;
+        if (any) {
             int at = -1, end = -1;  // of the rows before the lane's, and of the chunk
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -511,7 +523,8 @@ linattn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             }
             t.store(s.tab[c % NTAB]);
             tc::mbar_arrive(&s.tab_full[c % NTAB]);
-            total += t.total;
+            // (a segment with a border anywhere takes nothing over, whatever its other decays are)
+            total = total == -INFINITY || t.total == -INFINITY ? -INFINITY : total + t.total;
         }
         if (STATE && blockIdx.x == 0 && lane == 0) a.decays[(long long)item * a.H + h] = (float)total;
     } else if (warp == 3) {

@@ -443,3 +443,54 @@ def test_linear_attention_many_short_prompts_captured_of_other_key_dims(dt, dims
         graph.replay()
     _status_ok(hy, torch)
     assert torch.equal(o, o2) and torch.equal(end, end2)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dims", ALL_DIMS)
+@pytest.mark.parametrize("at,reset", [(0, 1), (5, 9), (10, 200), (63, 64), (20, 31), (130, 190)])
+def test_linear_attention_decay_that_is_no_number_before_a_reset(dt, dims, at, reset):
+    """A NaN or +infinity as a log decay reaches no row from the next one on that forgets everything."""
+    torch, hy, rt, code, tdt = _mods()
+    lens, Hk, H, (dk, dv) = [260, 40], 1, 2, dims
+    x = _linear(dt, lens, Hk, H, dk, dv, 218, decay=0.05)
+    q, k, v, g, st, cu = x
+    n = sum(lens)
+    g[reset] = g[reset + 30] = float("-inf")
+    want, oa, we, ea = ro.linear_attention(*(_np(t)[:n] for t in (q, k, v, g)), _offsets(lens), Hk, H, dk ** -0.5, _np(st))
+    ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
+    for bad in (float("nan"), float("inf")):
+        gg = g.clone()
+        gg[at] = bad
+        o, end = _run_linear(dt, x, Hk, H, dk, dv, True, g=gg)
+        _status_ok(hy, torch)
+        got = _np(o)[:n]
+        sees = np.zeros(n, dtype=bool)
+        sees[at:reset] = True
+        _hold(got[~sees], want[~sees], ob[~sees], f"{dt} {dims} {bad}, rows that do not see it")
+        assert not np.isfinite(got[sees]).any()
+        _hold(_np(end), we, eb, f"{dt} {dims} {bad} states")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("at,reset", [(400, 600), (600, 601), (600, 1500)])
+def test_linear_attention_few_long_prompts_decay_that_is_no_number(dt, at, reset):
+    """As above, in one segment of a long prompt and in two."""
+    torch, hy, rt, code, tdt = _mods()
+    lens, Hk, H, dk, dv = [2500, 30], 2, 2, 64, 64
+    x = _linear(dt, lens, Hk, H, dk, dv, 219, decay=0.01)
+    q, k, v, g, st, cu = x
+    n = sum(lens)
+    g[reset] = float("-inf")
+    want, oa, we, ea = ro.linear_attention(*(_np(t)[:n] for t in (q, k, v, g)), _offsets(lens), Hk, H, dk ** -0.5, _np(st))
+    ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
+    for bad in (float("nan"), float("inf")):
+        gg = g.clone()
+        gg[at] = bad
+        o, end = _run_linear(dt, x, Hk, H, dk, dv, True, g=gg)
+        _status_ok(hy, torch)
+        got = _np(o)[:n]
+        sees = np.zeros(n, dtype=bool)
+        sees[at:reset] = True
+        _hold(got[~sees], want[~sees], ob[~sees], f"{dt} {bad}, rows that do not see it")
+        assert not np.isfinite(got[sees]).any()
+        _hold(_np(end), we, eb, f"{dt} {bad} states")
