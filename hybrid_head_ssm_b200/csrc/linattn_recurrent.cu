@@ -7,9 +7,9 @@
 // of S in registers: LPR lanes per row, each with every LPR-th float4 of the key
 // dimension, so a warp's loads are whole 128-byte lines and a row's product with q is a
 // shuffle over LPR lanes. Single tokens are bound by HBM: 8 bytes per state element; 256 of 25
-// heads of 64 x 128 63.5 us (the copy rate), one 2.2 us. fp32 prompts are bound by the chain of rows (a
+// heads of 64 x 128 64.9 us called back to back (the copy rate), one 2.2 us. fp32 prompts are bound by the chain of rows (a
 // round trip to memory, 64 multiply-adds and a shuffle each): 185 rows 104 us, eight of up to 4224
-// rows 3933 us (their bytes take 118).
+// rows 3864 us (their bytes take 118).
 #include "kernels.h"
 #include "ragged.cuh"
 

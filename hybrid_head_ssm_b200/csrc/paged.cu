@@ -134,7 +134,7 @@ __device__ __forceinline__ long long slot_of(const DecodeArgs<T>& a, int b, int 
 // CUDA cores (fp32 rows): one 128-thread block per (key split, KV head and group of up to 8
 // of its query heads, sequence). Chunks of 128 keys: a thread forms one key's scores, two
 // heads' softmax per warp, then a thread owns a column of V. Bound by latency: nothing is in flight
-// across a chunk's barriers. 64 sequences in a window of 1024 240 us, 16 of up to 32896 1312 us (their
+// across a chunk's barriers. 64 sequences in a window of 1024 236 us, 16 of up to 32896 1287 us (their
 // bytes take 40 and 191).
 constexpr int SC = 128, SR = 8;
 constexpr int MAX_CL = 8;        // splits that join as one cluster
