@@ -329,8 +329,9 @@ int hymba_attn_decode_static(const hymba_layer_cfg* cfg, const void* q, int64_t 
  * HYMBA_F32. Products of 16-bit operands run on the tensor cores with fp32
  * accumulation, fp32 ones on the CUDA cores; softmax statistics and states are fp32.
  * Values at places that a row does not see, non-finite ones among them, do not reach
- * the row's output. An infinite value that it sees gives an infinity (or NaN, with others), which
- * takes a slower path than finite ones. All calls only queue work on `stream`: they can be captured into a
+ * the row's output. An infinite value that it sees gives an infinity (or NaN: with others, or
+ * where its weight is 0, as of a key whose score is -infinity), which takes a slower path than
+ * finite ones. All calls only queue work on `stream`: they can be captured into a
  * graph, and calls on different streams may overlap as long as they share no output and
  * no workspace.
  * --------------------------------------------------------------------------- */

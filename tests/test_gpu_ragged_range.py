@@ -279,7 +279,7 @@ def test_linear_attention_growth(dt, dims, grow):
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
-@pytest.mark.parametrize("dk,dv", [(16, 64), (128, 64)])
+@pytest.mark.parametrize("dk,dv", [(16, 64), (128, 64), (64, 64), (64, 128)])
 def test_linear_attention_value_columns_of_different_size(dt, dk, dv):
     """Value columns near 2^13 beside ones near 2^-13, decays of 2^-8 over a chunk: each column of the state
     keeps its own bits."""
@@ -494,3 +494,26 @@ def test_linear_attention_few_long_prompts_decay_that_is_no_number(dt, at, reset
         _hold(got[~sees], want[~sees], ob[~sees], f"{dt} {bad}, rows that do not see it")
         assert not np.isfinite(got[sees]).any()
         _hold(_np(end), we, eb, f"{dt} {bad} states")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("lens", [[2500], [1900, 2100]])
+@pytest.mark.parametrize("reset", [None, 777, 1279, 1280])
+def test_linear_attention_few_long_prompts_growth(dt, lens, reset):
+    """Growth over whole segments, a row that forgets everything within one, at its end and at the next one's
+    start; the output's scale brings the last rows back near 1."""
+    torch, hy, rt, code, tdt = _mods()
+    Hk, H, dk, dv = 1, 1, 64, 64
+    x = _linear(dt, lens, Hk, H, dk, dv, 220)
+    q, k, v, g, st, cu = x
+    g.copy_(0.03 * torch.rand(g.shape, generator=torch.Generator(device="cuda").manual_seed(221), device="cuda"))
+    if reset is not None:
+        g[reset] = float("-inf")
+    scale = float(np.exp(-0.015 * max(lens))) * dk ** -0.5
+    o, end = _run_linear(dt, x, Hk, H, dk, dv, True, scale=scale, in_place=True)
+    _status_ok(hy, torch)
+    n = sum(lens)
+    want, oa, we, ea = ro.linear_attention(*(_np(t)[:n] for t in (q, k, v, g)), _offsets(lens), Hk, H, scale, _np(st))
+    ob, eb = _linear_bounds(want, oa, we, ea, dt, max(lens), dk)
+    _hold(_np(o)[:n], want[:n], ob[:n], f"{dt} o")
+    _hold(_np(end), we, eb, f"{dt} state", 2.0 ** -16)
