@@ -26,8 +26,8 @@
 // the start of i's block and so at most 1 each (a chunk with a positive log decay forms
 // 2^(a_i + b_j) instead), within a block 2^(a_i + b_j). A row that forgets everything (a decay that is 0
 // in fp32) is no term of cs but a border that nothing before it passes and at which cs starts again, so
-// the distances stay small after any number of them (only decays of 2^-100 and less that are not 0, row after row, leave the others of
-// their block right to 2^-11, a step of P). K' enters as three parts (bf16: 24 bits) or two
+// the distances stay small after any number of them (only decays of 2^-100 and less that are not 0, row
+// after row, leave the others of their block right to 2^-11, a step of P). K' enters as three parts (bf16: 24 bits) or two
 // (fp16: 22 bits, or 2^-37 of the chunk's largest weighted key where that is more); P and the state's
 // copy are rounded to the rows' type, like any MMA operand. fp16 has little range: P's rows, the copy's rows and
 // K' are brought to the middle of it by powers of two that the fp32 values give back (the

@@ -390,8 +390,8 @@ typedef struct hymba_paged_kv {
  * its newest positions len[b] - n_b .. len[b] - 1: len already counts them (the caller
  * advances it, on the same stream, before the call). cu_seqlens NULL: one row per
  * sequence, total_rows = batch. A row whose position is negative, whose page is out of range or
- * whose sequence's len is past the table is not written and HYMBA_ERR_DEVICE_RANGE is recorded. Rows of two sequences that meet in one
- * slot race: one of them stays. */
+ * whose sequence's len is past the table is not written and HYMBA_ERR_DEVICE_RANGE is
+ * recorded. Rows of two sequences that meet in one slot race: one of them stays. */
 int hymba_kv_append_paged(const hymba_paged_kv* kv, const void* k, int64_t ldk, const void* v, int64_t ldv,
                           const int32_t* cu_seqlens, int total_rows, void* stream);
 
